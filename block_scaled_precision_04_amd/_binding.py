@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_HERE, "libbsgemm.so")
 BS_OP_FP8_BLOCK = 1
 BS_OP_W4A8_MXFP4 = 2
 BS_OP_BF16_SKINNY = 3
+BS_OP_W4A4_MXFP4 = 4
+BS_OP_MOE_SORT = 5
 BS_LAYOUT_FP8_BLOCK = 0x38423631
 BS_LAYOUT_MXFP4 = 0x34584D31
 BS_WDESC_MAGIC = 0x42534744
@@ -66,6 +68,15 @@ SIGNATURES = {
     "quant_fp8_per_token": (_I, [_P, _P, _P, _I, _I, _P]),
     "quant_fp8_group128": (_I, [_P, _P, _P, _I, _I, _P]),
     "quant_fp8_block128": (_I, [_P, _P, _P, _I, _I, _P]),
+    "bsgemm_w4a4_mxfp4": (_I, [_P, _L, _P, _L, _D, _P, _P, _L, _I, _I, _I, _P, _Z, _P]),
+    "bsgemm_w4a4_mxfp4_grouped": (_I, [_P, _L, _P, _L, _I, _P, _P, _D, _P, _Z, _P, _L, _I, _I, _I, _I, _P]),
+    "quant_mxfp4": (_I, [_P, _L, _P, _P, _I, _I, _P]),
+    "silu_mul_quant_mxfp4": (_I, [_P, _P, _P, _P, _I, _I, _P]),
+    "dequant_mxfp4": (_I, [_P, _P, _P, _I, _I, _P]),
+    "moe_sort": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _Z, _P]),
+    "moe_gather": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "moe_combine": (_I, [_P, _P, _P, _P, _I, _I, _I, _P]),
+    "moe_combine_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
 }
 
 _LIB = None
@@ -139,6 +150,21 @@ def _on_device(fn, *ts):
     _need(len(devs) <= 1, fn, f"tensors are on different devices: {sorted(map(str, devs))}")
 
 
+def _on_current(fn, *ts):
+    """Every tensor lives on the current GPU: the launch goes to its current stream."""
+    _on_device(fn, *ts)
+    for t in ts:
+        if t is not None:
+            cur = torch.cuda.current_device()
+            _need(t.device.index == cur, fn, f"tensors are on {t.device}, the current device is cuda:{cur}")
+            return
+
+
+def _row_stride(t):
+    """Leading dimension of a [M, C] tensor (with one row any stride is a dense one)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _ws(fn, ws):
     """(pointer, bytes) of an optional workspace tensor (dense, any dtype)."""
     if ws is None:
@@ -188,6 +214,29 @@ def prelayout_mxfp4(w_packed, w_e8m0):
     desc = WDesc()
     _check("bs_prelayout_mxfp4", lib().bs_prelayout_mxfp4(_ptr(wp), _ptr(e), _ptr(out), nbytes, N, K,
                                                            ctypes.byref(desc), _stream()))
+    return out, desc
+
+
+def prelayout_mxfp4_experts(w_packed, w_e8m0):
+    """[E, N, K/2] packed e2m1 + [E, N, K/32] e8m0 -> (uint8 [E, total_bytes] with
+    every expert's pre-laid-out weight, the WDesc that they share)."""
+    fn = "prelayout_mxfp4_experts"
+    _need(isinstance(w_packed, torch.Tensor) and w_packed.dim() == 3, fn, "w_packed must be a 3-D tensor [E, N, K/2]")
+    E, N, Kh = w_packed.shape
+    K = 2 * Kh
+    _need(E >= 1, fn, "at least one expert is needed")
+    _arg(fn, "w_packed", w_packed, (E, N, Kh), (torch.uint8,), unit_inner=False)
+    _arg(fn, "w_e8m0", w_e8m0, (E, N, K // 32), (torch.uint8,), unit_inner=False)
+    nbytes = lib().bs_prelayout_mxfp4_bytes(N, K)
+    if nbytes == 0:
+        raise BsError("bs_prelayout_mxfp4_bytes", -2)
+    _on_current(fn, w_packed, w_e8m0)
+    out = torch.empty((E, nbytes), dtype=torch.uint8, device=w_packed.device)
+    desc = WDesc()
+    for e in range(E):
+        wp, sc = w_packed[e].contiguous(), w_e8m0[e].contiguous()
+        _check(fn, lib().bs_prelayout_mxfp4(_ptr(wp), _ptr(sc), _ptr(out[e]), nbytes, N, K, ctypes.byref(desc),
+                                            _stream()))
     return out, desc
 
 
@@ -286,6 +335,69 @@ def bsgemm_w4a8_mxfp4_atiled(a_tiled, a_scale, desc, w_pre, M, out=None, ws=None
     _check(fn, lib().bsgemm_w4a8_mxfp4_atiled(
         _ptr(a_tiled), _ptr(a_scale.contiguous()), ctypes.byref(desc), _ptr(w_pre), _ptr(out), out.stride(0),
         M, N, K, ws_p, ws_n, _stream()))
+    return out
+
+
+def _mxfp4_activation(fn, a, a_scale, desc):
+    """Checked (a, a_scale, rows, K) of an MXFP4 activation: codes [M, K/2], scales [M, K/32]."""
+    _need(isinstance(a, torch.Tensor) and a.dim() == 2, fn, "a must be a 2-D tensor [M, K/2]")
+    M, Kh = a.shape
+    K = 2 * Kh
+    _need(desc.K == K, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
+    _arg(fn, "a", a, (M, Kh), (torch.uint8,))
+    _arg(fn, "a_scale", a_scale, (M, K // 32), (torch.uint8,))
+    return M, K
+
+
+def bsgemm_w4a4_mxfp4(a, a_scale, desc, w_pre, out=None, ws=None):
+    """C[M,N] bf16 = MXFP4 W4A4 GEMM.  a: [M, K/2] packed e2m1 (row stride in
+    bytes may be padded to a multiple of 16); a_scale: e8m0 [M, K/32] (row
+    stride padded to a multiple of 4); ws: alloc_workspace(BS_OP_W4A4_MXFP4, M, N, K)."""
+    fn = "bsgemm_w4a4_mxfp4"
+    M, K = _mxfp4_activation(fn, a, a_scale, desc)
+    N = desc.N
+    _need(isinstance(w_pre, torch.Tensor), fn, "w_pre must be a torch.Tensor")
+    _arg(fn, "w_pre", w_pre, (w_pre.numel(),), (torch.uint8,), contiguous=True)
+    _need(w_pre.numel() >= desc.total_bytes, fn, f"w_pre holds {w_pre.numel()} bytes, the layout needs "
+                                                 f"{desc.total_bytes}")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    _arg(fn, "out", out, (M, N), _BF16)
+    _on_current(fn, a, a_scale, w_pre, out, ws)
+    ws_p, ws_n = _ws(fn, ws)
+    _check(fn, lib().bsgemm_w4a4_mxfp4(
+        _ptr(a), _row_stride(a), _ptr(a_scale), _row_stride(a_scale), ctypes.byref(desc), _ptr(w_pre), _ptr(out),
+        _row_stride(out), M, N, K, ws_p, ws_n, _stream()))
+    return out
+
+
+def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=None):
+    """The experts' W4A4 products over slots sorted by expert (moe_sort):
+    out[s] = a[rows[s]] . W_e^T for offsets[e] <= s < offsets[e+1]; bf16 [S, N].
+    offsets: int32 [E+1]; rows: int32 [S] (None: slot s is row s of a); desc,
+    w_pre: from prelayout_mxfp4_experts.  Rows of out past offsets[E] keep what
+    they hold (pass out to choose; a fresh one is not cleared)."""
+    fn = "bsgemm_w4a4_mxfp4_grouped"
+    Ma, K = _mxfp4_activation(fn, a, a_scale, desc)
+    N = desc.N
+    _need(isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
+    E = w_pre.shape[0]
+    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), (torch.uint8,))
+    _need(w_pre.shape[1] >= desc.total_bytes, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs "
+                                                  f"{desc.total_bytes}")
+    _arg(fn, "offsets", offsets, (E + 1,), (torch.int32,), contiguous=True)
+    S = Ma
+    if rows is not None:
+        _need(isinstance(rows, torch.Tensor), fn, "rows must be a torch.Tensor")
+        S = rows.numel()
+        _arg(fn, "rows", rows, (S,), (torch.int32,), contiguous=True)
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=a.device)
+    _arg(fn, "out", out, (S, N), _BF16)
+    _on_current(fn, a, a_scale, offsets, w_pre, rows, out)
+    _check(fn, lib().bsgemm_w4a4_mxfp4_grouped(
+        _ptr(a), _row_stride(a), _ptr(a_scale), _row_stride(a_scale), Ma, _ptr(offsets), _ptr(rows),
+        ctypes.byref(desc), _ptr(w_pre), _row_stride(w_pre), _ptr(out), _row_stride(out), S, E, N, K, _stream()))
     return out
 
 
@@ -437,3 +549,148 @@ def quant_fp8_block128(w, q=None, scale=None):
     w, q, scale = _quant_args(fn, w, q, scale, (N, K), (N // 128, K // 128))
     _check(fn, lib().quant_fp8_block128(_ptr(w), _ptr(q), _ptr(scale), N, K, _stream()))
     return q, scale
+
+
+# ------------------------------------------------------------------ MXFP4 quantizers
+def _mxfp4_out(fn, q, scale, M, K, device):
+    q = torch.empty((M, K // 2), dtype=torch.uint8, device=device) if q is None else q
+    scale = torch.empty((M, K // 32), dtype=torch.uint8, device=device) if scale is None else scale
+    _arg(fn, "q", q, (M, K // 2), (torch.uint8,), contiguous=True)
+    _arg(fn, "scale", scale, (M, K // 32), (torch.uint8,), contiguous=True)
+    return q, scale
+
+
+def quant_mxfp4(x, q=None, scale=None):
+    """x bf16 [M, K] (row stride may be padded to a multiple of 8) ->
+    (q packed e2m1 uint8 [M, K/2], scale e8m0 uint8 [M, K/32])."""
+    fn = "quant_mxfp4"
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [M, K]")
+    M, K = x.shape
+    _need(K >= 32 and K % 32 == 0, fn, f"K = {K} must be a multiple of 32")
+    _arg(fn, "x", x, (M, K), _BF16, unit_inner=False)
+    q, scale = _mxfp4_out(fn, q, scale, M, K, x.device)
+    _on_current(fn, x, q, scale)
+    if x.stride(1) != 1 or (M > 1 and (x.stride(0) < K or x.stride(0) % 8)) or x.data_ptr() % 16:
+        x = x.contiguous() if not x.is_contiguous() else x.clone()
+    _check(fn, lib().quant_mxfp4(_ptr(x), _row_stride(x), _ptr(q), _ptr(scale), M, K, _stream()))
+    return q, scale
+
+
+def silu_mul_quant_mxfp4(gu, q=None, scale=None, rows=None):
+    """gu bf16 [M, 2N] (gate half first) -> (q packed e2m1 [M, N/2], scale e8m0
+    [M, N/32]) of silu(gate) * up.  rows: optional int32 tensor of one element;
+    only the first min(rows, M) rows are computed (e.g. offsets[E:])."""
+    fn = "silu_mul_quant_mxfp4"
+    _need(isinstance(gu, torch.Tensor) and gu.dim() == 2 and gu.shape[1] % 2 == 0, fn,
+          "gu must be a 2-D tensor [M, 2N]")
+    M, N = gu.shape[0], gu.shape[1] // 2
+    _need(N >= 32 and N % 32 == 0, fn, f"N = {N} must be a multiple of 32")
+    _arg(fn, "gu", gu, (M, 2 * N), _BF16, unit_inner=False)
+    if rows is not None:
+        _arg(fn, "rows", rows, (1,), (torch.int32,))
+    q, scale = _mxfp4_out(fn, q, scale, M, N, gu.device)
+    _on_current(fn, gu, q, scale, rows)
+    gu = gu.contiguous()
+    _check(fn, lib().silu_mul_quant_mxfp4(_ptr(gu), _ptr(q), _ptr(scale), _ptr(rows), M, N, _stream()))
+    return q, scale
+
+
+def dequant_mxfp4(q, scale, out=None):
+    """(q packed e2m1 [M, K/2], scale e8m0 [M, K/32]) -> the values, bf16 [M, K]."""
+    fn = "dequant_mxfp4"
+    _need(isinstance(q, torch.Tensor) and q.dim() == 2, fn, "q must be a 2-D tensor [M, K/2]")
+    M, K = q.shape[0], 2 * q.shape[1]
+    _need(K >= 32 and K % 32 == 0, fn, f"K = {K} must be a multiple of 32")
+    _arg(fn, "q", q, (M, K // 2), (torch.uint8,), unit_inner=False)
+    _arg(fn, "scale", scale, (M, K // 32), (torch.uint8,), unit_inner=False)
+    out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device) if out is None else out
+    _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
+    _on_current(fn, q, scale, out)
+    q, scale = q.contiguous(), scale.contiguous()
+    _check(fn, lib().dequant_mxfp4(_ptr(q), _ptr(scale), _ptr(out), M, K, _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ mixture of experts
+def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
+    """Sort the (token, expert) pairs by expert.  ids: int32 [T, k], ids outside
+    [0, E) are dropped.  -> (rows int32 [T*k]: token of each slot, -1 past the
+    kept pairs; pos int32 [T, k]: slot of each pair, -1 if dropped; offsets int32
+    [E+1]).  ws: alloc_workspace(BS_OP_MOE_SORT, T, k, E)."""
+    fn = "moe_sort"
+    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, fn, "ids must be a 2-D tensor [T, k]")
+    T, k = ids.shape
+    _arg(fn, "ids", ids, (T, k), (torch.int32,), unit_inner=False)
+    dev = ids.device
+    rows = torch.empty((T * k,), dtype=torch.int32, device=dev) if rows is None else rows
+    pos = torch.empty((T, k), dtype=torch.int32, device=dev) if pos is None else pos
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev) if offsets is None else offsets
+    _arg(fn, "rows", rows, (T * k,), (torch.int32,), contiguous=True)
+    _arg(fn, "pos", pos, (T, k), (torch.int32,), contiguous=True)
+    _arg(fn, "offsets", offsets, (E + 1,), (torch.int32,), contiguous=True)
+    _on_current(fn, ids, rows, pos, offsets, ws)
+    ids = ids.contiguous()
+    ws_p, ws_n = _ws(fn, ws)
+    _check(fn, lib().moe_sort(_ptr(ids), _ptr(rows), _ptr(pos), _ptr(offsets), T, k, E, ws_p, ws_n, _stream()))
+    return rows, pos, offsets
+
+
+def _moe_pos(fn, pos):
+    _need(isinstance(pos, torch.Tensor) and pos.dim() == 2, fn, "pos must be a 2-D tensor [T, k]")
+    _arg(fn, "pos", pos, tuple(pos.shape), (torch.int32,), contiguous=True)
+    return pos.shape
+
+
+def moe_gather(x, pos, out=None):
+    """Token rows in slot order: out[pos[t, j]] = x[t], bf16 [T*k, K].  Rows that
+    no pair names keep what they hold.  Gradient: moe_combine(d_out, pos)."""
+    fn = "moe_gather"
+    T, k = _moe_pos(fn, pos)
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [T, K]")
+    K = x.shape[1]
+    _arg(fn, "x", x, (T, K), _BF16, unit_inner=False)
+    out = torch.empty((T * k, K), dtype=torch.bfloat16, device=x.device) if out is None else out
+    _arg(fn, "out", out, (T * k, K), _BF16, contiguous=True)
+    _on_current(fn, x, pos, out)
+    x = x.contiguous()
+    _check(fn, lib().moe_gather(_ptr(x), _ptr(pos), _ptr(out), T, k, K, _stream()))
+    return out
+
+
+def moe_combine(y, pos, weights=None, out=None):
+    """out[t] = sum_j weights[t, j] * y[pos[t, j]], bf16 [T, K]; weights fp32
+    [T, k] or None for ones.  Dropped pairs (pos -1) add nothing."""
+    fn = "moe_combine"
+    T, k = _moe_pos(fn, pos)
+    _need(isinstance(y, torch.Tensor) and y.dim() == 2, fn, "y must be a 2-D tensor [T*k, K]")
+    K = y.shape[1]
+    _arg(fn, "y", y, (T * k, K), _BF16, unit_inner=False)
+    if weights is not None:
+        _arg(fn, "weights", weights, (T, k), (torch.float32,), contiguous=True)
+    out = torch.empty((T, K), dtype=torch.bfloat16, device=y.device) if out is None else out
+    _arg(fn, "out", out, (T, K), _BF16, contiguous=True)
+    _on_current(fn, y, pos, weights, out)
+    y = y.contiguous()
+    _check(fn, lib().moe_combine(_ptr(y), _ptr(pos), _ptr(weights), _ptr(out), T, k, K, _stream()))
+    return out
+
+
+def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None):
+    """Gradient of moe_combine: (dy bf16 [T*k, K] with dy[pos[t, j]] =
+    weights[t, j] * dout[t], other rows as they were; dweights fp32 [T, k])."""
+    fn = "moe_combine_backward"
+    T, k = _moe_pos(fn, pos)
+    _need(isinstance(dout, torch.Tensor) and dout.dim() == 2, fn, "dout must be a 2-D tensor [T, K]")
+    K = dout.shape[1]
+    _arg(fn, "dout", dout, (T, K), _BF16, unit_inner=False)
+    _arg(fn, "y", y, (T * k, K), _BF16, unit_inner=False)
+    _arg(fn, "weights", weights, (T, k), (torch.float32,), contiguous=True)
+    dy = torch.empty((T * k, K), dtype=torch.bfloat16, device=y.device) if dy is None else dy
+    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device) if dweights is None else dweights
+    _arg(fn, "dy", dy, (T * k, K), _BF16, contiguous=True)
+    _arg(fn, "dweights", dweights, (T, k), (torch.float32,), contiguous=True)
+    _on_current(fn, dout, y, pos, weights, dy, dweights)
+    dout, y = dout.contiguous(), y.contiguous()
+    _check(fn, lib().moe_combine_backward(_ptr(dout), _ptr(y), _ptr(pos), _ptr(weights), _ptr(dy), _ptr(dweights),
+                                          T, k, K, _stream()))
+    return dy, dweights

@@ -19,11 +19,19 @@ size_t bs_prefill_workspace(int M, int N, int K);
 int bs_launch_skinny(const uint16_t* x, const uint16_t* w, uint16_t* c, int M, int N, int K, void* ws,
                      hipStream_t st);
 size_t bs_skinny_workspace(int M, int N, int K);
+int bs_launch_w4a4(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const uint8_t* w, size_t w_scales,
+                   uint16_t* c, int64_t ldc, int M, int N, int K, void* ws, hipStream_t st);
+int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const int* offsets,
+                           const int* rows, const uint8_t* w, size_t w_scales, size_t w_stride, uint16_t* c,
+                           int64_t ldc, int S, int Ma, int E, int N, int K, hipStream_t st);
+size_t bs_w4a4_workspace(int M, int N, int K);
+size_t bs_moe_sort_workspace(int T, int k, int E);
 
 namespace {
 constexpr int kW4A8DecodeMaxM = 64;  // above this the compute-bound tiled kernel runs
 constexpr int kSkinnyMaxM = 64;
 constexpr int kFp8MaxM = 1 << 20;
+constexpr int kMaxExperts = 1024;
 
 // A split-K launch needs a workspace of at least `need` bytes, 256-aligned.
 int check_workspace(size_t need, const void* ws, size_t ws_bytes) {
@@ -87,6 +95,11 @@ BS_API size_t bs_workspace_bytes(int op, int M, int N, int K) {
     if (M < 1 || M > (1 << 22) || N < 16 || N % 16 || K < 128 || K % 128) return 0;
     return M <= kW4A8DecodeMaxM ? bs_decode_workspace(M, N, K, true) : bs_prefill_workspace(M, N, K);
   }
+  if (op == BS_OP_W4A4_MXFP4) {
+    if (M < 1 || M > (1 << 22) || N < 16 || N % 16 || K < 128 || K % 128) return 0;
+    return bs_w4a4_workspace(M, N, K);
+  }
+  if (op == BS_OP_MOE_SORT) return bs_moe_sort_workspace(M, N, K);
   return 0;
 }
 
@@ -172,6 +185,54 @@ BS_API int bsgemm_w4a8_mxfp4_atiled(const void* a_tiled, const float* a_scale, c
   return bs_launch_w4a8_prefill(static_cast<const uint8_t*>(a_tiled), K, a_scale, w,
                                 reinterpret_cast<const uint32_t*>(w + wd->scales_offset), static_cast<uint16_t*>(c),
                                 ldc, M, N, K, ws, true, static_cast<hipStream_t>(stream));
+}
+
+BS_API int bsgemm_w4a4_mxfp4(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, const bs_wdesc* wd,
+                             const void* w_pre, void* c, int64_t ldc, int M, int N, int K, void* ws, size_t ws_bytes,
+                             bs_stream_t stream) {
+  if (M == 0) return BS_OK;  // an empty batch: nothing is read or launched
+  BS_CHECK(a && a_scale && wd && w_pre && c, BS_ERR_NULL);
+  BS_CHECK(M >= 1 && M <= (1 << 22) && N >= 16 && N % 16 == 0 && K >= 128 && K % 128 == 0, BS_ERR_SHAPE);
+  BS_CHECK(mx_desc_ok(wd, N, K), BS_ERR_LAYOUT);
+  BS_CHECK(lda >= K / 2 && lda % 16 == 0 && ld_scale >= K / 32 && ld_scale % 4 == 0 && ldc >= N && ldc % 4 == 0,
+           BS_ERR_ALIGN);
+  BS_CHECK(bs_aligned(a, 16) && bs_aligned(a_scale, 4) && bs_aligned(w_pre, 256) && bs_aligned(c, 16), BS_ERR_ALIGN);
+  // the activation rows, their scales and the weight codes are addressed with
+  // unsigned 32-bit offsets
+  BS_CHECK(lda < (1ll << 32) && ld_scale < (1ll << 32) && static_cast<uint64_t>(M) * lda < (1ull << 32) &&
+               static_cast<uint64_t>(M) * ld_scale < (1ull << 32) &&
+               static_cast<uint64_t>(N) * static_cast<uint64_t>(K) / 2 < (1ull << 32),
+           BS_ERR_SHAPE);
+  const int wst = check_workspace(bs_w4a4_workspace(M, N, K), ws, ws_bytes);
+  if (wst != BS_OK) return wst;
+  return bs_launch_w4a4(static_cast<const uint8_t*>(a), lda, static_cast<const uint8_t*>(a_scale), ld_scale,
+                        static_cast<const uint8_t*>(w_pre), wd->scales_offset, static_cast<uint16_t*>(c), ldc, M, N, K,
+                        ws, static_cast<hipStream_t>(stream));
+}
+
+BS_API int bsgemm_w4a4_mxfp4_grouped(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, int Ma,
+                                     const int32_t* offsets, const int32_t* rows, const bs_wdesc* wd,
+                                     const void* w_pre, size_t w_stride, void* c, int64_t ldc, int S, int E, int N,
+                                     int K, bs_stream_t stream) {
+  if (S == 0) return BS_OK;  // no slots: nothing is read or launched
+  BS_CHECK(a && a_scale && offsets && wd && w_pre && c, BS_ERR_NULL);
+  BS_CHECK(S >= 1 && S <= (1 << 24) && Ma >= 1 && E >= 1 && E <= kMaxExperts && N >= 16 && N % 16 == 0 && K >= 128 &&
+               K % 128 == 0,
+           BS_ERR_SHAPE);
+  BS_CHECK(mx_desc_ok(wd, N, K), BS_ERR_LAYOUT);
+  BS_CHECK(w_stride >= wd->total_bytes && w_stride % 256 == 0, BS_ERR_LAYOUT);
+  BS_CHECK(lda >= K / 2 && lda % 16 == 0 && ld_scale >= K / 32 && ld_scale % 4 == 0 && ldc >= N && ldc % 4 == 0,
+           BS_ERR_ALIGN);
+  BS_CHECK(bs_aligned(a, 16) && bs_aligned(a_scale, 4) && bs_aligned(w_pre, 256) && bs_aligned(c, 16) &&
+               bs_aligned(offsets, 4) && bs_aligned(rows, 4),
+           BS_ERR_ALIGN);
+  BS_CHECK(lda < (1ll << 32) && ld_scale < (1ll << 32) && static_cast<uint64_t>(Ma) * lda < (1ull << 32) &&
+               static_cast<uint64_t>(Ma) * ld_scale < (1ull << 32) &&
+               static_cast<uint64_t>(N) * static_cast<uint64_t>(K) / 2 < (1ull << 32),
+           BS_ERR_SHAPE);
+  return bs_launch_w4a4_grouped(static_cast<const uint8_t*>(a), lda, static_cast<const uint8_t*>(a_scale), ld_scale,
+                                offsets, rows, static_cast<const uint8_t*>(w_pre), wd->scales_offset, w_stride,
+                                static_cast<uint16_t*>(c), ldc, S, Ma, E, N, K, static_cast<hipStream_t>(stream));
 }
 
 BS_API int gemm_bf16_skinny(const void* x, const void* w, void* c, int M, int N, int K, void* ws, size_t ws_bytes,

@@ -9,8 +9,9 @@
  * failed check the call returns a negative status and enqueues nothing.  A
  * launch failure returns BS_ERR_LAUNCH.  No C++ exception crosses this ABI.
  * A call with zero rows (M == 0 for the GEMMs, producers and activation
- * quantizers) is an empty batch: it returns BS_OK before reading any other
- * argument (pointers may be NULL) and launches nothing.
+ * quantizers, S == 0 for the grouped GEMM, T == 0 for the row moves of the
+ * mixture of experts) is an empty batch: it returns BS_OK before reading any
+ * other argument (pointers may be NULL) and launches nothing.
  * The library keeps no state between calls and is safe to call from several
  * host threads.
  *
@@ -146,7 +147,13 @@ BS_API int bs_unprelayout_mxfp4(const bs_wdesc* desc, const void* pre, void* w_p
  * instructions and each workgroup waits for its partial stores to be
  * acknowledged before it bumps the counter with a device-scope atomic.  The
  * test suite pins that encoding in the compiled kernels. */
-enum { BS_OP_FP8_BLOCK = 1, BS_OP_W4A8_MXFP4 = 2, BS_OP_BF16_SKINNY = 3 };
+enum {
+  BS_OP_FP8_BLOCK = 1,
+  BS_OP_W4A8_MXFP4 = 2,
+  BS_OP_BF16_SKINNY = 3,
+  BS_OP_W4A4_MXFP4 = 4,
+  BS_OP_MOE_SORT = 5 /* M, N, K = tokens, experts per token, experts */
+};
 BS_API size_t bs_workspace_bytes(int op, int M, int N, int K);
 
 /* ------------------------------------------------------------- GEMMs */
@@ -248,6 +255,45 @@ BS_API int gemm_bf16_skinny(const void* x, const void* w, void* c, int M, int N,
 BS_API int gemm_bf16_skinny_noalloc(const void* x, const void* w, void* c, int M, int N, int K,
                                     bs_stream_t stream);
 
+/* MXFP4 W4A4 GEMM: both operands e2m1 with one e8m0 scale per 32 along K (the
+ * radiance_mxfp4.py page's checkpoint format has MXFP4 activations; its own
+ * kernel runs them as e4m3, bsgemm_w4a8_mxfp4):
+ *   C[m,n] = bf16( sum_k a[m,k] * 2^(EA[m,k/32]-127) * w[n,k] * 2^(EW[n,k/32]-127) )
+ * accumulated in fp32.  A scale byte of 255 is NaN: every product that it
+ * enters is NaN.
+ * a: packed e2m1 [M, K/2] (even k in the low nibble; lda bytes, multiple of
+ * 16); a_scale: e8m0 [M, K/32] (ld_scale bytes, multiple of 4): what
+ * quant_mxfp4 and silu_mul_quant_mxfp4 write; w_pre: pre-laid-out by
+ * bs_prelayout_mxfp4 (desc wd), the same buffer that bsgemm_w4a8_mxfp4 takes;
+ * c: bf16 [M, N] (ldc elements, multiple of 4).  Needs 1 <= M <= 2^22,
+ * N % 16 == 0, K % 128 == 0; a, c 16-byte, a_scale 4-byte, w_pre 256-byte
+ * aligned; M * lda, M * ld_scale and N * K / 2 < 2^32.
+ * Up to 64 rows a weight stream runs, above an LDS-tiled kernel; either may
+ * split K through ws of bs_workspace_bytes(BS_OP_W4A4_MXFP4, M, N, K) bytes
+ * (256-byte aligned, zeroed once); when that is 0, ws may be NULL. */
+BS_API int bsgemm_w4a4_mxfp4(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, const bs_wdesc* wd,
+                             const void* w_pre, void* c, int64_t ldc, int M, int N, int K, void* ws, size_t ws_bytes,
+                             bs_stream_t stream);
+
+/* The same product for the experts of a mixture, over slots sorted by expert
+ * (moe_sort): expert e has the slots offsets[e] .. offsets[e+1]-1 and the
+ * weight at w_pre + e * w_stride, and
+ *   C[s,:] = A[rows[s],:] . W_e^T     for offsets[e] <= s < offsets[e+1]
+ * a, a_scale: as above with Ma rows; offsets: int32 [E+1], not decreasing,
+ * from 0 on, at most S; rows: int32 [S], the source row of each slot, or NULL
+ * when slot s is row s of a.  wd describes one expert's weight (all have the
+ * same shape); w_stride: bytes from one to the next, a multiple of 256, at
+ * least wd->total_bytes.  c: bf16 [S, N]; the rows of slots past offsets[E]
+ * are left as they are.  offsets and rows are read on the device only: the
+ * call does not wait for them.  Values out of range name no memory outside
+ * the buffers (offsets are clamped to [0, S], rows to [0, Ma)) but give
+ * undefined results.  Needs 1 <= E <= 1024, S <= 2^24 (S == 0 is an empty
+ * batch) and the alignments and limits above with Ma for M.  No workspace. */
+BS_API int bsgemm_w4a4_mxfp4_grouped(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, int Ma,
+                                     const int32_t* offsets, const int32_t* rows, const bs_wdesc* wd,
+                                     const void* w_pre, size_t w_stride, void* c, int64_t ldc, int S, int E, int N,
+                                     int K, bs_stream_t stream);
+
 /* ----------------------------------------------------------- producers */
 
 /* Fused residual add + Gemma RMSNorm + per-token e4m3 quant (radiance_arnq.py
@@ -313,6 +359,77 @@ BS_API int quant_fp8_group128(const void* x, void* q, float* scale, int M, int K
  * w: bf16 [N, K]; q: e4m3 [N, K]; scale: fp32 [N/128, K/128].
  * N % 128 == 0, K % 128 == 0. */
 BS_API int quant_fp8_block128(const void* w, void* q, float* scale, int N, int K, bs_stream_t stream);
+
+/* MXFP4 quant of bf16 rows: one e8m0 scale per 32 consecutive values (the OCP
+ * microscaling rule; the activation and weight format of the pages' checkpoint):
+ *   e = clamp(floor(log2(max |x|)) - 2, -127, 127) over the 32 values
+ *   q = e2m1(x / 2^e), round to nearest even, magnitudes above 6 to 6
+ *   scale byte = e + 127
+ * exact (the codes are the definition's, bit for bit).  A block with an
+ * infinity or a NaN gets the scale byte 255 (NaN) and zero codes; an all-zero
+ * block the byte 0.
+ * x: bf16 [M, K] (ldx elements, multiple of 8); q: packed e2m1 [M, K/2] (even
+ * k in the low nibble); scale: e8m0 [M, K/32]; both dense, the inputs of
+ * bsgemm_w4a4_mxfp4 and (for a weight) of bs_prelayout_mxfp4.  K % 32 == 0,
+ * M * K / 8 < 2^31; x 16-byte, q 4-byte aligned. */
+BS_API int quant_mxfp4(const void* x, int64_t ldx, void* q, void* scale, int M, int K, bs_stream_t stream);
+
+/* SiLU(gate) * up + the same quant (as silu_mul_quant_fp8, for the MXFP4
+ * consumer):  h = fp32(g / (1 + exp(-g)) * u), the real value rounded once,
+ * g = gu[m, k], u = gu[m, N + k]; then quant_mxfp4's rule on h.  The codes are
+ * those of the correctly rounded h.  gu: bf16 [M, 2N] contiguous (gate half
+ * first); q: [M, N/2]; scale: [M, N/32].  rows: NULL, or a device int32: only
+ * the first min(*rows, M) rows are computed and the rest left as they are (for
+ * slots sorted by expert, offsets + E).  N % 32 == 0, M * N / 8 < 2^31; gu
+ * 16-byte, q and rows 4-byte aligned.  No overlap between gu and the outputs. */
+BS_API int silu_mul_quant_mxfp4(const void* gu, void* q, void* scale, const int32_t* rows, int M, int N,
+                                bs_stream_t stream);
+
+/* The values that MXFP4 codes stand for: out[m, k] = e2m1(q[m, k]) *
+ * 2^(scale[m, k/32] - 127), bf16 [M, K] dense (exact; beyond bf16's range an
+ * infinity; NaN where the scale byte is 255).  K % 32 == 0, M * K / 8 < 2^31;
+ * q 4-byte, out 16-byte aligned. */
+BS_API int dequant_mxfp4(const void* q, const void* scale, void* out, int M, int K, bs_stream_t stream);
+
+/* ------------------------------------------------- mixture of experts
+ * Pair p = t * k + j is the j-th choice of token t.  Every sum below runs in
+ * the order of j and every result is deterministic. */
+
+/* Sort the pairs by expert (stable: equal ids keep the order of p).
+ * ids: int32 [T, k]; a pair whose id is outside [0, E) is dropped (a padded
+ * token, an expert of another rank).  The kept pairs take the slots 0, 1, ...
+ * in the order of (id, p):
+ *   offsets[e]  int32 [E+1]   first slot of expert e; offsets[E] = kept pairs
+ *   pos[p]      int32 [T, k]  slot of pair p, -1 if dropped
+ *   rows[s]     int32 [T * k] token of slot s, -1 for s >= offsets[E]
+ * An expert may be chosen more than once by a token.  T >= 0 (with T == 0 only
+ * offsets is written, with zeros), 1 <= E <= 1024, T * k <= 2^24.  More than
+ * 8192 pairs need ws of bs_workspace_bytes(BS_OP_MOE_SORT, T, k, E) bytes
+ * (256-byte aligned; shared and zeroed like the other workspaces). */
+BS_API int moe_sort(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* offsets, int T, int k, int E, void* ws,
+                    size_t ws_bytes, bs_stream_t stream);
+
+/* Token rows in slot order: xs[pos[t, j], :] = x[t, :] for every kept pair;
+ * rows of xs that no pair names are left as they are.  x: bf16 [T, K]; xs:
+ * bf16 [T * k, K]; dense, 16-byte aligned.  K % 8 == 0, K <= 32768,
+ * T * k <= 2^24, T * K / 8 < 2^31 (here and below).  Entries of pos outside
+ * [0, T * k) count as dropped.  Its gradient is moe_combine with weights NULL. */
+BS_API int moe_gather(const void* x, const int32_t* pos, void* xs, int T, int k, int K, bs_stream_t stream);
+
+/* Expert rows back in token order: out[t, :] = bf16( sum_j weights[t, j] *
+ * y[pos[t, j], :] ) over the kept pairs, fp32; zero for a token without any.
+ * y: bf16 [T * k, K]; weights: fp32 [T, k], or NULL for ones; out: bf16 [T, K].
+ * Rows of dropped pairs are not used. */
+BS_API int moe_combine(const void* y, const int32_t* pos, const float* weights, void* out, int T, int k, int K,
+                       bs_stream_t stream);
+
+/* The gradient of moe_combine for dout = d/d out (bf16 [T, K]):
+ *   dy[pos[t, j], :] = bf16( weights[t, j] * dout[t, :] )   other rows of dy are left as they are
+ *   dweights[t, j]   = sum_c dout[t, c] * y[pos[t, j], c]   fp32; 0 for a dropped pair
+ * pos has to name every slot at most once, as moe_sort writes it.  No overlap
+ * between inputs and outputs. */
+BS_API int moe_combine_backward(const void* dout, const void* y, const int32_t* pos, const float* weights, void* dy,
+                                float* dweights, int T, int k, int K, bs_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,9 +19,10 @@ Modules
   quant     the pages' per-token quant and the block / group fixture quantizers
   layout    the weight pre-layout index maps (gfx950 MFMA fragment order)
   checks    the tolerance checks used by the parity tests
+  mxfp4     MXFP4 quantisation, the W4A4 product, expert routing and its gradient
 
 Parity pins live in tests/test_oracle_*.py.  Every function here is pinned to
 something other than itself (closed forms, the pages' printed tables,
 library conversions, exact rational brute force); none is "parity unpinned".
 """
-from . import codecs, gemm, producer, quant, layout, checks  # noqa: F401
+from . import codecs, gemm, producer, quant, layout, checks, mxfp4  # noqa: F401
