@@ -104,11 +104,18 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
+
+
+# The raw handle of a device's current stream; torch's Stream object costs about
+# 3 us to build, as much as the whole C call of a small operator.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _u8(t):
@@ -121,6 +128,9 @@ def _u8(t):
 # otherwise be written as if it were a dense [M, N] buffer.
 _FP8 = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_U8 = (torch.uint8,)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
 
 
 def _need(cond, fn, msg):
@@ -131,12 +141,17 @@ def _need(cond, fn, msg):
 def _arg(fn, name, t, shape, dtypes, contiguous=False, unit_inner=True):
     """t must have `shape` and one of `dtypes`; its last dimension must be
     unit-stride (rows may be padded) or, with contiguous=True, the tensor dense."""
-    _need(t is not None, fn, f"{name} is required")
-    _need(isinstance(t, torch.Tensor), fn, f"{name} must be a torch.Tensor")
-    _need(t.dtype in dtypes, fn, f"{name} has dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
-    _need(tuple(t.shape) == tuple(shape), fn, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    # an accepted tensor builds no message: formatting one for every argument
+    # took most of a small call's host time
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape):
+        _need(t is not None, fn, f"{name} is required")
+        _need(isinstance(t, torch.Tensor), fn, f"{name} must be a torch.Tensor")
+        _need(t.dtype in dtypes, fn, f"{name} has dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
+        _need(tuple(t.shape) == tuple(shape), fn, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t
     if contiguous:
-        _need(t.is_contiguous(), fn, f"{name} must be contiguous")
+        _need(False, fn, f"{name} must be contiguous")
     elif unit_inner and t.dim() >= 2 and t.shape[-1] > 1:
         _need(t.stride(-1) == 1, fn, f"{name} must have unit stride along its last dimension")
         _need(t.stride(0) >= t.shape[-1], fn, f"{name} rows overlap (stride {t.stride(0)} < {t.shape[-1]})")
@@ -145,19 +160,25 @@ def _arg(fn, name, t, shape, dtypes, contiguous=False, unit_inner=True):
 
 def _on_device(fn, *ts):
     """Every tensor lives on the same GPU (a host tensor would hand the kernels a host address)."""
-    devs = {t.device for t in ts if t is not None}
-    _need(all(d.type == "cuda" for d in devs), fn, f"tensors must be on a GPU, got {sorted(map(str, devs))}")
-    _need(len(devs) <= 1, fn, f"tensors are on different devices: {sorted(map(str, devs))}")
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if first is None:
+            first = t.device
+        if t.device != first or first.type != "cuda":
+            devs = {u.device for u in ts if u is not None}
+            _need(all(d.type == "cuda" for d in devs), fn, f"tensors must be on a GPU, got {sorted(map(str, devs))}")
+            _need(False, fn, f"tensors are on different devices: {sorted(map(str, devs))}")
+    return first
 
 
 def _on_current(fn, *ts):
     """Every tensor lives on the current GPU: the launch goes to its current stream."""
-    _on_device(fn, *ts)
-    for t in ts:
-        if t is not None:
-            cur = torch.cuda.current_device()
-            _need(t.device.index == cur, fn, f"tensors are on {t.device}, the current device is cuda:{cur}")
-            return
+    dev = _on_device(fn, *ts)
+    cur = torch.cuda.current_device()
+    if dev.index != cur:
+        _need(False, fn, f"tensors are on {dev}, the current device is cuda:{cur}")
 
 
 def _row_stride(t):
@@ -343,9 +364,10 @@ def _mxfp4_activation(fn, a, a_scale, desc):
     _need(isinstance(a, torch.Tensor) and a.dim() == 2, fn, "a must be a 2-D tensor [M, K/2]")
     M, Kh = a.shape
     K = 2 * Kh
-    _need(desc.K == K, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
-    _arg(fn, "a", a, (M, Kh), (torch.uint8,))
-    _arg(fn, "a_scale", a_scale, (M, K // 32), (torch.uint8,))
+    if desc.K != K:
+        _need(False, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
+    _arg(fn, "a", a, (M, Kh), _U8)
+    _arg(fn, "a_scale", a_scale, (M, K // 32), _U8)
     return M, K
 
 
@@ -357,12 +379,13 @@ def bsgemm_w4a4_mxfp4(a, a_scale, desc, w_pre, out=None, ws=None):
     M, K = _mxfp4_activation(fn, a, a_scale, desc)
     N = desc.N
     _need(isinstance(w_pre, torch.Tensor), fn, "w_pre must be a torch.Tensor")
-    _arg(fn, "w_pre", w_pre, (w_pre.numel(),), (torch.uint8,), contiguous=True)
-    _need(w_pre.numel() >= desc.total_bytes, fn, f"w_pre holds {w_pre.numel()} bytes, the layout needs "
-                                                 f"{desc.total_bytes}")
+    _arg(fn, "w_pre", w_pre, (w_pre.numel(),), _U8, contiguous=True)
+    if w_pre.numel() < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {w_pre.numel()} bytes, the layout needs {desc.total_bytes}")
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
-    _arg(fn, "out", out, (M, N), _BF16)
+    else:
+        _arg(fn, "out", out, (M, N), _BF16)
     _on_current(fn, a, a_scale, w_pre, out, ws)
     ws_p, ws_n = _ws(fn, ws)
     _check(fn, lib().bsgemm_w4a4_mxfp4(
@@ -382,18 +405,19 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
     N = desc.N
     _need(isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
     E = w_pre.shape[0]
-    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), (torch.uint8,))
-    _need(w_pre.shape[1] >= desc.total_bytes, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs "
-                                                  f"{desc.total_bytes}")
-    _arg(fn, "offsets", offsets, (E + 1,), (torch.int32,), contiguous=True)
+    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), _U8)
+    if w_pre.shape[1] < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs {desc.total_bytes}")
+    _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
     S = Ma
     if rows is not None:
         _need(isinstance(rows, torch.Tensor), fn, "rows must be a torch.Tensor")
         S = rows.numel()
-        _arg(fn, "rows", rows, (S,), (torch.int32,), contiguous=True)
+        _arg(fn, "rows", rows, (S,), _I32, contiguous=True)
     if out is None:
         out = torch.empty((S, N), dtype=torch.bfloat16, device=a.device)
-    _arg(fn, "out", out, (S, N), _BF16)
+    else:
+        _arg(fn, "out", out, (S, N), _BF16)
     _on_current(fn, a, a_scale, offsets, w_pre, rows, out)
     _check(fn, lib().bsgemm_w4a4_mxfp4_grouped(
         _ptr(a), _row_stride(a), _ptr(a_scale), _row_stride(a_scale), Ma, _ptr(offsets), _ptr(rows),
@@ -455,7 +479,7 @@ def _producer_args(fn, y, residual, gamma, q, scale, residual_out, group):
     scale = torch.empty(sshape, dtype=torch.float32, device=dev) if scale is None else scale
     residual_out = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if residual_out is None else residual_out
     _arg(fn, "q", q, (M, K), _FP8, contiguous=True)
-    _arg(fn, "scale", scale, sshape, (torch.float32,), contiguous=True)
+    _arg(fn, "scale", scale, sshape, _F32, contiguous=True)
     _arg(fn, "residual_out", residual_out, (M, K), _BF16, contiguous=True)
     _on_device(fn, y, residual, gamma, q, scale, residual_out)
     return y.contiguous(), residual.contiguous(), gamma.contiguous(), q, scale, residual_out
@@ -467,7 +491,7 @@ def _quant_args(fn, x, q, scale, qshape, sshape, in_shape=None):
     q = torch.empty(qshape, dtype=torch.uint8, device=x.device) if q is None else q
     scale = torch.empty(sshape, dtype=torch.float32, device=x.device) if scale is None else scale
     _arg(fn, "q", q, qshape, _FP8, contiguous=True)
-    _arg(fn, "scale", scale, sshape, (torch.float32,), contiguous=True)
+    _arg(fn, "scale", scale, sshape, _F32, contiguous=True)
     _on_device(fn, x, q, scale)
     return x.contiguous(), q, scale
 
@@ -553,10 +577,14 @@ def quant_fp8_block128(w, q=None, scale=None):
 
 # ------------------------------------------------------------------ MXFP4 quantizers
 def _mxfp4_out(fn, q, scale, M, K, device):
-    q = torch.empty((M, K // 2), dtype=torch.uint8, device=device) if q is None else q
-    scale = torch.empty((M, K // 32), dtype=torch.uint8, device=device) if scale is None else scale
-    _arg(fn, "q", q, (M, K // 2), (torch.uint8,), contiguous=True)
-    _arg(fn, "scale", scale, (M, K // 32), (torch.uint8,), contiguous=True)
+    if q is None:
+        q = torch.empty((M, K // 2), dtype=torch.uint8, device=device)
+    else:
+        _arg(fn, "q", q, (M, K // 2), _U8, contiguous=True)
+    if scale is None:
+        scale = torch.empty((M, K // 32), dtype=torch.uint8, device=device)
+    else:
+        _arg(fn, "scale", scale, (M, K // 32), _U8, contiguous=True)
     return q, scale
 
 
@@ -566,12 +594,13 @@ def quant_mxfp4(x, q=None, scale=None):
     fn = "quant_mxfp4"
     _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [M, K]")
     M, K = x.shape
-    _need(K >= 32 and K % 32 == 0, fn, f"K = {K} must be a multiple of 32")
+    if K < 32 or K % 32:
+        _need(False, fn, f"K = {K} must be a multiple of 32")
     _arg(fn, "x", x, (M, K), _BF16, unit_inner=False)
     q, scale = _mxfp4_out(fn, q, scale, M, K, x.device)
     _on_current(fn, x, q, scale)
     if x.stride(1) != 1 or (M > 1 and (x.stride(0) < K or x.stride(0) % 8)) or x.data_ptr() % 16:
-        x = x.contiguous() if not x.is_contiguous() else x.clone()
+        x = x.clone(memory_format=torch.contiguous_format)
     _check(fn, lib().quant_mxfp4(_ptr(x), _row_stride(x), _ptr(q), _ptr(scale), M, K, _stream()))
     return q, scale
 
@@ -584,10 +613,11 @@ def silu_mul_quant_mxfp4(gu, q=None, scale=None, rows=None):
     _need(isinstance(gu, torch.Tensor) and gu.dim() == 2 and gu.shape[1] % 2 == 0, fn,
           "gu must be a 2-D tensor [M, 2N]")
     M, N = gu.shape[0], gu.shape[1] // 2
-    _need(N >= 32 and N % 32 == 0, fn, f"N = {N} must be a multiple of 32")
+    if N < 32 or N % 32:
+        _need(False, fn, f"N = {N} must be a multiple of 32")
     _arg(fn, "gu", gu, (M, 2 * N), _BF16, unit_inner=False)
     if rows is not None:
-        _arg(fn, "rows", rows, (1,), (torch.int32,))
+        _arg(fn, "rows", rows, (1,), _I32)
     q, scale = _mxfp4_out(fn, q, scale, M, N, gu.device)
     _on_current(fn, gu, q, scale, rows)
     gu = gu.contiguous()
@@ -600,11 +630,14 @@ def dequant_mxfp4(q, scale, out=None):
     fn = "dequant_mxfp4"
     _need(isinstance(q, torch.Tensor) and q.dim() == 2, fn, "q must be a 2-D tensor [M, K/2]")
     M, K = q.shape[0], 2 * q.shape[1]
-    _need(K >= 32 and K % 32 == 0, fn, f"K = {K} must be a multiple of 32")
-    _arg(fn, "q", q, (M, K // 2), (torch.uint8,), unit_inner=False)
-    _arg(fn, "scale", scale, (M, K // 32), (torch.uint8,), unit_inner=False)
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device) if out is None else out
-    _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
+    if K < 32 or K % 32:
+        _need(False, fn, f"K = {K} must be a multiple of 32")
+    _arg(fn, "q", q, (M, K // 2), _U8, unit_inner=False)
+    _arg(fn, "scale", scale, (M, K // 32), _U8, unit_inner=False)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
+    else:
+        _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
     _on_current(fn, q, scale, out)
     q, scale = q.contiguous(), scale.contiguous()
     _check(fn, lib().dequant_mxfp4(_ptr(q), _ptr(scale), _ptr(out), M, K, _stream()))
@@ -620,14 +653,20 @@ def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
     fn = "moe_sort"
     _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, fn, "ids must be a 2-D tensor [T, k]")
     T, k = ids.shape
-    _arg(fn, "ids", ids, (T, k), (torch.int32,), unit_inner=False)
+    _arg(fn, "ids", ids, (T, k), _I32, unit_inner=False)
     dev = ids.device
-    rows = torch.empty((T * k,), dtype=torch.int32, device=dev) if rows is None else rows
-    pos = torch.empty((T, k), dtype=torch.int32, device=dev) if pos is None else pos
-    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev) if offsets is None else offsets
-    _arg(fn, "rows", rows, (T * k,), (torch.int32,), contiguous=True)
-    _arg(fn, "pos", pos, (T, k), (torch.int32,), contiguous=True)
-    _arg(fn, "offsets", offsets, (E + 1,), (torch.int32,), contiguous=True)
+    if rows is None:
+        rows = torch.empty((T * k,), dtype=torch.int32, device=dev)
+    else:
+        _arg(fn, "rows", rows, (T * k,), _I32, contiguous=True)
+    if pos is None:
+        pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    else:
+        _arg(fn, "pos", pos, (T, k), _I32, contiguous=True)
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    else:
+        _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
     _on_current(fn, ids, rows, pos, offsets, ws)
     ids = ids.contiguous()
     ws_p, ws_n = _ws(fn, ws)
@@ -637,7 +676,7 @@ def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
 
 def _moe_pos(fn, pos):
     _need(isinstance(pos, torch.Tensor) and pos.dim() == 2, fn, "pos must be a 2-D tensor [T, k]")
-    _arg(fn, "pos", pos, tuple(pos.shape), (torch.int32,), contiguous=True)
+    _arg(fn, "pos", pos, tuple(pos.shape), _I32, contiguous=True)
     return pos.shape
 
 
@@ -649,8 +688,10 @@ def moe_gather(x, pos, out=None):
     _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [T, K]")
     K = x.shape[1]
     _arg(fn, "x", x, (T, K), _BF16, unit_inner=False)
-    out = torch.empty((T * k, K), dtype=torch.bfloat16, device=x.device) if out is None else out
-    _arg(fn, "out", out, (T * k, K), _BF16, contiguous=True)
+    if out is None:
+        out = torch.empty((T * k, K), dtype=torch.bfloat16, device=x.device)
+    else:
+        _arg(fn, "out", out, (T * k, K), _BF16, contiguous=True)
     _on_current(fn, x, pos, out)
     x = x.contiguous()
     _check(fn, lib().moe_gather(_ptr(x), _ptr(pos), _ptr(out), T, k, K, _stream()))
@@ -666,9 +707,11 @@ def moe_combine(y, pos, weights=None, out=None):
     K = y.shape[1]
     _arg(fn, "y", y, (T * k, K), _BF16, unit_inner=False)
     if weights is not None:
-        _arg(fn, "weights", weights, (T, k), (torch.float32,), contiguous=True)
-    out = torch.empty((T, K), dtype=torch.bfloat16, device=y.device) if out is None else out
-    _arg(fn, "out", out, (T, K), _BF16, contiguous=True)
+        _arg(fn, "weights", weights, (T, k), _F32, contiguous=True)
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.bfloat16, device=y.device)
+    else:
+        _arg(fn, "out", out, (T, K), _BF16, contiguous=True)
     _on_current(fn, y, pos, weights, out)
     y = y.contiguous()
     _check(fn, lib().moe_combine(_ptr(y), _ptr(pos), _ptr(weights), _ptr(out), T, k, K, _stream()))
@@ -684,11 +727,15 @@ def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None):
     K = dout.shape[1]
     _arg(fn, "dout", dout, (T, K), _BF16, unit_inner=False)
     _arg(fn, "y", y, (T * k, K), _BF16, unit_inner=False)
-    _arg(fn, "weights", weights, (T, k), (torch.float32,), contiguous=True)
-    dy = torch.empty((T * k, K), dtype=torch.bfloat16, device=y.device) if dy is None else dy
-    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device) if dweights is None else dweights
-    _arg(fn, "dy", dy, (T * k, K), _BF16, contiguous=True)
-    _arg(fn, "dweights", dweights, (T, k), (torch.float32,), contiguous=True)
+    _arg(fn, "weights", weights, (T, k), _F32, contiguous=True)
+    if dy is None:
+        dy = torch.empty((T * k, K), dtype=torch.bfloat16, device=y.device)
+    else:
+        _arg(fn, "dy", dy, (T * k, K), _BF16, contiguous=True)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    else:
+        _arg(fn, "dweights", dweights, (T, k), _F32, contiguous=True)
     _on_current(fn, dout, y, pos, weights, dy, dweights)
     dout, y = dout.contiguous(), y.contiguous()
     _check(fn, lib().moe_combine_backward(_ptr(dout), _ptr(y), _ptr(pos), _ptr(weights), _ptr(dy), _ptr(dweights),
