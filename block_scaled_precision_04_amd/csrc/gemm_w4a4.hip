@@ -16,6 +16,7 @@
 // never waits for them; the activation rows are read through the sorted order
 // (row gather in the loads), never copied.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
@@ -305,40 +306,56 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 // ========================================================= many rows: LDS tiles
 // A workgroup computes a BM x BN tile with WM x WN waves, each (BM/WM) x
 // (BN/WN) as 32x32 sub-tiles; first MFMA operand the weight (rows = n), second
-// the activation, so a lane holds four consecutive n of one m.  K advances in
-// 128-wide steps; a step's activation codes (BM x 64 B, chunks swizzled by
-// swz4), weight codes (BN/16 fragment blocks of 1 KiB, as they are), weight
-// scale dwords (256 B per 16 columns, four steps) and activation scale dwords
-// (one per row) go global -> LDS by direct loads into one of STAGES buffers.
-template <int BM, int BN, int WM, int WN, int STAGES_>
+// the activation, so a lane holds four consecutive n of one m.
+//
+// K advances in 128-wide steps, four to a window.  A step's activation codes
+// (BM x 64 B, chunks swizzled by swz4) and weight codes (BN/16 fragment blocks
+// of 1 KiB, as they are) go global -> LDS by direct loads into one of four
+// stage buffers; the scales of a window (16 B per activation row, 256 B per 16
+// columns) into one of two window buffers.  The four steps of a window are
+// unrolled, so the stage, the scale dword and its byte are constants of the
+// code, and a window's scales are read from LDS once, ahead of the window.
+//
+// AS16: the activation scale rows are 16-byte aligned and K is a multiple of
+// 512, so a row's window is one 16-byte load (rows of 16 B); otherwise it is
+// four 4-byte loads (planes of BM dwords).  One 4-byte load per row and step
+// touched as many cache lines per step as the codes themselves.
+template <int BM, int BN, int WM, int WN, bool AS16>
 struct TileCfg {
-  static constexpr int kStages = STAGES_;
+  static constexpr int kStages = 4;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kTM = BM / WM / 32, kTN = BN / WN / 32;
-  static constexpr int kA = BM * 64, kB = BN * 64, kSB = BN * 16, kSA = BM * 4;
-  static constexpr int kStage = kA + kB + kSB + kSA;
+  static constexpr int kA = BM * 64, kB = BN * 64, kStage = kA + kB;
+  static constexpr int kSB = BN * 16, kSA = BM * 16, kWin = kSB + kSA;
+  static constexpr int kWin0 = kStages * kStage;       // the window buffers follow the stages
   static constexpr int kAIters = kA / (kThreads * 16), kBIters = kB / (kThreads * 16);
-  static constexpr int kSBPieces = kSB / 1024, kSAPieces = kSA / 256;
-  // loads per stage, the same for every wave: a wave past a section's last
-  // piece repeats an earlier one (same bytes, same place)
+  static constexpr int kSBPieces = kSB / 1024, kSAPieces = AS16 ? kSA / 1024 : kSA / 256;
+  // loads per stage and per window, the same for every wave: a wave past a
+  // section's last piece repeats an earlier one (same bytes, same place)
   static constexpr int kSBIters = (kSBPieces + kWaves - 1) / kWaves, kSAIters = (kSAPieces + kWaves - 1) / kWaves;
-  static constexpr int kDma = kAIters + kBIters + kSBIters + kSAIters;
-  static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 256 == 0, "");
+  static constexpr int kDma = kAIters + kBIters, kWinDma = kSBIters + kSAIters;
+  static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
   static constexpr int kPassN = BN < 128 ? BN : 128;   // columns staged at once by the epilogue
-  static constexpr int kLds = std::max(kStages * kStage, BM * kPassN * 4);
+  static constexpr int kMain = kWin0 + 2 * kWin;
+  static constexpr int kLds = kMain > BM * kPassN * 4 ? kMain : BM * kPassN * 4;
 };
 
-template <int BM, int BN, int WM, int WN, int STAGES, int OCC, bool GROUPED, bool SPLIT>
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+template <int BM, int BN, int WM, int WN, int OCC, bool GROUPED, bool SPLIT, bool AS16>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int group_m) {
-  using C = TileCfg<BM, BN, WM, WN, STAGES>;
+  using C = TileCfg<BM, BN, WM, WN, AS16>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int N = p.N, KS = p.KS, NT = N >> 4, KQ = (KS + 3) >> 2;
   const int n_tiles = (N + BN - 1) / BN;
+  // K splits cut between windows
   const int S = SPLIT ? static_cast<int>(gridDim.y) : 1, sp = SPLIT ? static_cast<int>(blockIdx.y) : 0;
-  const int k_begin = SPLIT ? KS * sp / S : 0, k_end = SPLIT ? KS * (sp + 1) / S : KS;
+  const int w_begin = SPLIT ? KQ * sp / S : 0, w_end = SPLIT ? KQ * (sp + 1) / S : KQ;
+  const int k_last = min(4 * w_end, KS) - 1;
 
   int m0, nrows, nt;
   const uint8_t* w = p.w;
@@ -379,28 +396,34 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
     sboff[i] = static_cast<uint32_t>(min(nt0 + (q >> 4), NT - 1)) * static_cast<uint32_t>(KQ) * 256u +
                static_cast<uint32_t>((q & 15) * 16);
   }
+  // AS16: piece = 64 rows; else piece = (dword j, 64 rows), j outermost
 #pragma unroll
   for (int i = 0; i < C::kSAIters; ++i) {
-    int src = m0 + min(((i * C::kWaves + wave) % C::kSAPieces) * 64 + l, nrows - 1);
+    const int pc = (i * C::kWaves + wave) % C::kSAPieces;
+    int src = m0 + min((AS16 ? pc : pc % (BM / 64)) * 64 + l, nrows - 1);
     if constexpr (GROUPED) src = src_row(p, src);
     saoff[i] = static_cast<uint32_t>(src) * p.lds;
   }
-  // the i-th load of step ks into buffer buf
-  auto dma_one = [&](int i, int ks, int buf) {
-    const uint32_t base = lds0 + buf * C::kStage;
-    if (i < C::kAIters) {
+  // the i-th load of step ks into stage st
+  auto dma_one = [&](int i, int ks, int st) {
+    const uint32_t base = lds0 + st * C::kStage;
+    if (i < C::kAIters)
       dma16(base + (i * C::kWaves + wave) * 1024, p.a + static_cast<size_t>(ks) * 64, aoff[i]);
-    } else if (i < C::kAIters + C::kBIters) {
-      const int j = i - C::kAIters;
-      dma16(base + C::kA + (j * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024, boff_g[j]);
-    } else if (i < C::kAIters + C::kBIters + C::kSBIters) {
-      const int j = i - C::kAIters - C::kBIters;
-      dma16(base + C::kA + C::kB + ((j * C::kWaves + wave) % C::kSBPieces) * 1024,
-            wsc + static_cast<size_t>(ks >> 2) * 256, sboff[j]);
+    else
+      dma16(base + C::kA + ((i - C::kAIters) * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024,
+            boff_g[i - C::kAIters]);
+  };
+  // the i-th load of window win into its buffer
+  auto win_one = [&](int i, int win) {
+    const uint32_t base = lds0 + C::kWin0 + (win & 1) * C::kWin;
+    if (i < C::kSBIters) {
+      dma16(base + ((i * C::kWaves + wave) % C::kSBPieces) * 1024, wsc + static_cast<size_t>(win) * 256, sboff[i]);
     } else {
-      const int j = i - C::kAIters - C::kBIters - C::kSBIters;
-      dma4(base + C::kA + C::kB + C::kSB + ((j * C::kWaves + wave) % C::kSAPieces) * 256,
-           p.as + static_cast<size_t>(ks) * 4, saoff[j]);
+      const int j = i - C::kSBIters, pc = (j * C::kWaves + wave) % C::kSAPieces;
+      if constexpr (AS16)
+        dma16(base + C::kSB + pc * 1024, p.as + static_cast<size_t>(win) * 16, saoff[j]);
+      else
+        dma4(base + C::kSB + pc * 256, p.as + static_cast<size_t>(min(4 * win + pc / (BM / 64), KS - 1)) * 4, saoff[j]);
     }
   };
 
@@ -412,99 +435,136 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
 
   // fragment places within a stage.  Weight sub-tile i, half hh: lane l takes
   // column l%32, K block 2hh + l/32; activation sub-tile j: row l%32, the same.
-  int boff[C::kTN][2], sbo[C::kTN][2], aofs[C::kTM][2], sao[C::kTM], arow[C::kTM];
+  const int nlane = (l & 15) + 16 * (l >> 5);         // within a 1 KiB block, half 0
+  const int bbase = C::kA + (wn * (BN / WN / 16) + ((l >> 4) & 1)) * 1024 + nlane * 16;
+  const int sbbase = (wn * (BN / WN / 16) + ((l >> 4) & 1)) * 256 + nlane * 4;
+  int arow[C::kTM], abase[2];
 #pragma unroll
-  for (int i = 0; i < C::kTN; ++i) {
-    const int nl = wn * (BN / WN) + 32 * i + (l & 31);
+  for (int j = 0; j < C::kTM; ++j) arow[j] = wm * (BM / WM) + 32 * j + (l & 31);
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int lane = (nl & 15) + 16 * (2 * hh + (l >> 5));
-      boff[i][hh] = C::kA + (nl >> 4) * 1024 + lane * 16;
-      sbo[i][hh] = C::kA + C::kB + (nl >> 4) * 256 + lane * 4;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < C::kTM; ++j) {
-    arow[j] = wm * (BM / WM) + 32 * j + (l & 31);
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) aofs[j][hh] = arow[j] * 64 + 16 * swz4(arow[j], 2 * hh + (l >> 5));
-    sao[j] = C::kA + C::kB + C::kSB + arow[j] * 4;
-  }
+  for (int hh = 0; hh < 2; ++hh) abase[hh] = arow[0] * 64 + 16 * swz4(arow[0], 2 * hh + (l >> 5));
   const int sh_a = 8 * (l >> 5);   // the lane's K block of a half is byte 2hh + l/32
 
   struct Frag {
     v4i b[C::kTN], a[C::kTM];
-    uint32_t sb[C::kTN], sa[C::kTM];
+  };
+  struct Scale {
+    int b[C::kTN][2];   // byte j: step j of the window
+    int a[C::kTM][4];   // dword j: step j; byte 2hh after the shift by sh_a
   };
   constexpr int kPieces = C::kTN + C::kTM;
-  // LDS read piece i of half hh: weight 0, the activations, the other weights
-  auto piece = [&](const uint8_t* st, int hh, Frag& f, int i) {
+  // LDS read piece i of half hh of stage st: weight 0, the activations, the other weights
+  auto piece = [&](int st, int hh, Frag& f, int i) {
+    const uint8_t* base = lds + st * C::kStage;
     if (i == 0 || i > C::kTM) {
       const int t = i == 0 ? 0 : i - C::kTM;
-      f.b[t] = *reinterpret_cast<const v4i*>(st + boff[t][hh]);
-      f.sb[t] = *reinterpret_cast<const uint32_t*>(st + sbo[t][hh]);
+      f.b[t] = *reinterpret_cast<const v4i*>(base + bbase + t * 2048 + hh * 512);
     } else {
-      const int t = i - 1;
-      f.a[t] = *reinterpret_cast<const v4i*>(st + aofs[t][hh]);
-      f.sa[t] = *reinterpret_cast<const uint32_t*>(st + sao[t]) >> sh_a;
+      f.a[i - 1] = *reinterpret_cast<const v4i*>(base + abase[hh] + (i - 1) * 2048);
     }
   };
-  // MFMAs of a half step; after MFMA i: load i of step dks into dbuf (if DMA)
-  // and read piece i of the next half
-  auto half = [&](const Frag& f, int sh, auto hh, auto dma, int dks, int dbuf, const uint8_t* rst, int rhh, Frag& rf) {
-    constexpr int HH = decltype(hh)::value;
-    constexpr bool DMA = decltype(dma)::value;
+  auto read_scale = [&](int win, Scale& s, int i) {
+    const uint8_t* base = lds + C::kWin0 + (win & 1) * C::kWin;
+    if (i < C::kTN) {
 #pragma unroll
-    for (int i = 0; i < C::kTN; ++i) {
-      const int sc = static_cast<int>(f.sb[i] >> sh);
-      const v8i bw = v8i{f.b[i][0], f.b[i][1], f.b[i][2], f.b[i][3], 0, 0, 0, 0};
+      for (int hh = 0; hh < 2; ++hh) s.b[i][hh] = *reinterpret_cast<const int*>(base + sbbase + i * 512 + hh * 128);
+    } else {
+      const int t = i - C::kTN;
+      if constexpr (AS16) {
+        const v4i v = *reinterpret_cast<const v4i*>(base + C::kSB + arow[t] * 16);
 #pragma unroll
-      for (int j = 0; j < C::kTM; ++j) {
-        const v8i aw = v8i{f.a[j][0], f.a[j][1], f.a[j][2], f.a[j][3], 0, 0, 0, 0};
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bw, aw, acc[i][j], 4, 4, 0, sc, 2 * HH,
-                                                                    static_cast<int>(f.sa[j]));
-        const int n = i * C::kTM + j;
-        __builtin_amdgcn_sched_barrier(0);
-        if (DMA && n < C::kDma) dma_one(n, dks, dbuf);
-        if (n < kPieces) piece(rst, rhh, rf, n);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < 4; ++j) s.a[t][j] = v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s.a[t][j] = *reinterpret_cast<const int*>(base + C::kSB + (j * BM + arow[t]) * 4);
       }
     }
+  };
+  auto shift_scale = [&](Scale& s) {
 #pragma unroll
-    for (int n = C::kTN * C::kTM; n < C::kDma; ++n)
-      if (DMA) dma_one(n, dks, dbuf);
+    for (int t = 0; t < C::kTM; ++t)
 #pragma unroll
-    for (int n = C::kTN * C::kTM; n < kPieces; ++n) piece(rst, rhh, rf, n);
+      for (int j = 0; j < 4; ++j) s.a[t][j] = static_cast<int>(static_cast<uint32_t>(s.a[t][j]) >> sh_a);
+  };
+  // MFMAs of half HH of step J of a window.  Between them: the LDS reads of the
+  // next half (rf, from stage rst, half rhh), this half's share of the loads of
+  // step dks (into stage (J + 3) % 4), of the next window's scale loads (J = 0)
+  // and, in the window's last half, the reads of the next window's scales.
+  auto half = [&](auto jj, auto hh, const Frag& f, const Scale& s, int rst, int rhh, Frag& rf, int dks, int win,
+                  int next_win, Scale& ns) {
+    constexpr int J = decltype(jj)::value, HH = decltype(hh)::value;
+    constexpr int kN = C::kTN * C::kTM;
+    constexpr int d0 = HH * ((C::kDma + 1) / 2), d1 = HH ? C::kDma : (C::kDma + 1) / 2;
+    (void)win;
+#pragma unroll
+    for (int n = 0; n < kN || n < kPieces; ++n) {
+      if (n < kN) {
+        const int i = n / C::kTM, j = n % C::kTM;
+        const v8i bw = v8i{f.b[i][0], f.b[i][1], f.b[i][2], f.b[i][3], 0, 0, 0, 0};
+        const v8i aw = v8i{f.a[j][0], f.a[j][1], f.a[j][2], f.a[j][3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bw, aw, acc[i][j], 4, 4, J, s.b[i][HH], 2 * HH,
+                                                                    s.a[j][J]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (n < kPieces) piece(rst, rhh, rf, n);
+      // the loads, spread evenly over the half's MFMAs
+#pragma unroll
+      for (int d = d0; d < d1; ++d)
+        if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, (J + 3) & 3);
+      if (J == 0 && HH == 1 && n == kN - 1)
+#pragma unroll
+        for (int d = 0; d < C::kWinDma; ++d) win_one(d, next_win);
+      if (J == 3 && HH == 1) {
+#pragma unroll
+        for (int d = 0; d < kPieces; ++d)
+          if (d * kN / kPieces == n) read_scale(next_win, ns, d);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   // Step s: this wave's loads of step s+1 have landed and its LDS reads are
-  // done; barrier (s+1 published, the buffer of s-1 free); MFMAs of the first
-  // half, with the loads of step s+STAGES-1 (into s-1's buffer) and the reads
-  // of the second half; MFMAs of the second half with the reads of the first
-  // half of s+1.  Steps past the end re-load the last one (never used).
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s)
-#pragma unroll
-    for (int i = 0; i < C::kDma; ++i) dma_one(i, min(k_begin + s, k_end - 1), s);
-  wait_vm<(STAGES - 2) * C::kDma>();
-  __syncthreads();
+  // done; barrier (s+1 published, the stage of s-1 free); then the two halves.
+  // The loads of a step are issued three steps ahead.  Steps past the end
+  // re-load the last one (never used).
   Frag f0, f1;
+  Scale s0, s1;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) piece(lds, 0, f0, i);
-  int buf = 0;
-  for (int ks = k_begin; ks < k_end; ++ks) {
-    const int sh = 8 * (ks & 3);
-    const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
-    const int pbuf = buf == 0 ? STAGES - 1 : buf - 1;
-    wait_vm<(STAGES - 3) * C::kDma>();
+  for (int d = 0; d < C::kWinDma; ++d) win_one(d, w_begin);
+#pragma unroll
+  for (int s = 0; s < 3; ++s)
+#pragma unroll
+    for (int i = 0; i < C::kDma; ++i) dma_one(i, min(4 * w_begin + s, k_last), s);
+  wait_vm<2 * C::kDma>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) piece(0, 0, f0, i);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) read_scale(w_begin, s0, i);
+  auto step = [&](auto jj, int win, Scale& s, Scale& ns) {
+    constexpr int J = decltype(jj)::value;
+    const int ks = 4 * win + J, next = min(win + 1, w_end - 1);
+    // newer loads that may be outstanding: those of step s+2, and the window's
+    // scale loads when they were issued after them (in step 0)
+    wait_vm<C::kDma + (J == 1 ? C::kWinDma : 0)>();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    half(f0, sh, std::integral_constant<int, 0>{}, std::true_type{}, min(ks + STAGES - 1, k_end - 1), pbuf,
-         lds + buf * C::kStage, 1, f1);
-    half(f1, sh, std::integral_constant<int, 1>{}, std::false_type{}, 0, 0, lds + nbuf * C::kStage, 0, f0);
-    __builtin_amdgcn_sched_barrier(0);
-    buf = nbuf;
+    if constexpr (J == 0) shift_scale(s);
+    half(jj, Int<0>{}, f0, s, J, 1, f1, min(ks + 3, k_last), win, next, ns);
+    half(jj, Int<1>{}, f1, s, (J + 1) & 3, 0, f0, min(ks + 3, k_last), win, next, ns);
+  };
+  // two windows per turn, so the scale sets swap without copies
+  auto window = [&](int win, Scale& s, Scale& ns) {
+    step(Int<0>{}, win, s, ns);
+    if (4 * win + 1 <= k_last) step(Int<1>{}, win, s, ns);
+    if (4 * win + 2 <= k_last) step(Int<2>{}, win, s, ns);
+    if (4 * win + 3 <= k_last) step(Int<3>{}, win, s, ns);
+  };
+  for (int win = w_begin; win < w_end; win += 2) {
+    window(win, s0, s1);
+    if (win + 1 < w_end) window(win + 1, s1, s0);
   }
   wait_vm<0>();
 
@@ -679,20 +739,26 @@ TilePlan tile_plan(int M, int N, int KS) {
   if (big >= 192) return TilePlan{true, big, 1};
   const int t = ((M + 127) / 128) * ((N + 127) / 128);
   const int s = t < 256 ? std::max(1, std::min(256 / t, KS / 8)) : 1;
-  return TilePlan{false, t, std::min(s, 0x7FFFFFFF / KS)};
+  return TilePlan{false, t, s};
 }
+
+// One 16-byte load per row and window of activation scales (see TileCfg).
+bool scales16(const W4A4Args& p) { return p.KS % 4 == 0 && p.lds % 16 == 0 && bs_aligned(p.as, 16); }
 
 int run_dense_tile(W4A4Args& p, void* ws, hipStream_t st) {
   const TilePlan pl = tile_plan(p.M, p.N, p.KS);
+  const bool as16 = scales16(p);
   if (pl.large) {
-    k_w4a4_tile<256, 256, 2, 2, 4, 1, false, false><<<dim3(pl.tiles, 1), 256, 0, st>>>(p, 4);
+    if (as16) k_w4a4_tile<256, 256, 2, 2, 1, false, false, true><<<dim3(pl.tiles, 1), 256, 0, st>>>(p, 4);
+    else k_w4a4_tile<256, 256, 2, 2, 1, false, false, false><<<dim3(pl.tiles, 1), 256, 0, st>>>(p, 4);
     return bs_launch_status();
   }
   if (pl.s > 1) {
     p.counters = static_cast<int*>(ws);
     p.slab = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
   }
-  k_w4a4_tile<128, 128, 2, 2, 4, 2, false, true><<<dim3(pl.tiles, pl.s), 256, 0, st>>>(p, 4);
+  if (as16) k_w4a4_tile<128, 128, 2, 2, 2, false, true, true><<<dim3(pl.tiles, pl.s), 256, 0, st>>>(p, 4);
+  else k_w4a4_tile<128, 128, 2, 2, 2, false, true, false><<<dim3(pl.tiles, pl.s), 256, 0, st>>>(p, 4);
   return bs_launch_status();
 }
 
@@ -749,6 +815,9 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
   if (avg <= 48) return launch_stream<4, 4, 2, 1, 4, true>(grouped_stream_cfg(S, E, N, p.KS, 4), p, st);
   const int64_t wgs = static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 127) / 128);
   if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
-  k_w4a4_tile<128, 128, 2, 2, 4, 2, true, false><<<dim3(static_cast<uint32_t>(wgs)), 256, 0, st>>>(p, 0);
+  if (scales16(p))
+    k_w4a4_tile<128, 128, 2, 2, 2, true, false, true><<<dim3(static_cast<uint32_t>(wgs)), 256, 0, st>>>(p, 0);
+  else
+    k_w4a4_tile<128, 128, 2, 2, 2, true, false, false><<<dim3(static_cast<uint32_t>(wgs)), 256, 0, st>>>(p, 0);
   return bs_launch_status();
 }
