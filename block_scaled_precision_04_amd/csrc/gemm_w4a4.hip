@@ -16,6 +16,7 @@
 // never waits for them; the activation rows are read through the sorted order
 // (row gather in the loads), never copied.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -26,8 +27,8 @@ struct W4A4Args {
   const uint8_t* a;      // e2m1 codes [rows, K/2], lda bytes apart
   const uint8_t* as;     // e8m0 [rows, K/32], lds bytes apart
   uint32_t lda, lds;
-  const uint8_t* w;      // pre-laid-out weight(s)
-  size_t w_scales;       // byte offset of the e8m0 section
+  const uint8_t* w;      // pre-laid-out weight(s): codes
+  const uint8_t* wsc;    // and e8m0 section
   size_t w_stride;       // grouped: bytes from one expert's weight to the next
   uint16_t* c;
   int64_t ldc;
@@ -40,6 +41,18 @@ struct W4A4Args {
   float* slab;
   int* counters;
 };
+
+// Inclusive sum over the wave's lanes: within rows of 16 by row shifts, then row
+// totals broadcast to the rows after (DPP moves, no LDS round trips).
+BS_INLINE int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row 0 -> 1, 2 -> 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // rows 0-1 -> 2-3
+  return v;
+}
 
 // The `tile`-th row tile of the grouped problem: the slots of expert e are cut
 // into runs of up to BM.  Lane l looks at experts 4l .. 4l+3 of each 256; a
@@ -59,12 +72,7 @@ BS_INLINE bool find_tile(const int* __restrict__ offsets, int E, int S, int tile
       cnt[i] = o[i + 1] > o[i] ? (o[i + 1] - o[i] + BM - 1) / BM : 0;
       mine += cnt[i];
     }
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      incl += l >= d ? v : 0;
-    }
+    const int incl = wave_scan(mine);
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (tile < run + total) {
       int before = run + incl - mine;
@@ -130,17 +138,18 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
   const int tile0 = (blockIdx.x * TW + tw) * T;
 
   int m0, nrows;
-  const uint8_t* w = p.w;
+  const uint8_t *w = p.w, *wscb = p.wsc;
   if constexpr (GROUPED) {
     int e, r1;
     if (!find_tile<16 * MB>(p.offsets, p.E, p.M, blockIdx.y, e, m0, r1)) return;
     nrows = r1 - m0;
     w += static_cast<size_t>(e) * p.w_stride;
+    wscb += static_cast<size_t>(e) * p.w_stride;
   } else {
     m0 = blockIdx.y * 16 * MB;
     nrows = min(RS, p.M - m0);
   }
-  const uint32_t* wsc = reinterpret_cast<const uint32_t*>(w + p.w_scales);
+  const uint32_t* wsc = reinterpret_cast<const uint32_t*>(wscb);
 
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
   const int a_instr = (kSteps * RS * 4 + 63) >> 6, s_instr = (kSteps * RS + 63) >> 6;
@@ -153,14 +162,15 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) acc[t][mb] = v4f{0, 0, 0, 0};
 
-  for (int it = 0; it < p.iters; ++it) {
-    const int wg_k0 = (blockIdx.z * p.iters + it) * kSteps;
-    if (wg_k0 >= KS) break;
+  const int iters = GROUPED ? p.iters : 1;   // (the loop costs the dense form register copies)
+  for (int it = 0; it < iters; ++it) {
+    const int wg_k0 = (blockIdx.z * iters + it) * kSteps;
+    if (GROUPED && wg_k0 >= KS) break;
     const int wg_steps = min(kSteps, KS - wg_k0);
     const int ks0 = wg_k0 + kw * R;
     const int klast = min(ks0 + R, KS) - 1;  // below ks0 for an idle wave
     const int nsteps = klast - ks0 + 1;      // <= 0 for an idle wave
-    if (it) __syncthreads();                 // every wave is done with the slice
+    if (GROUPED && it) __syncthreads();                 // every wave is done with the slice
     // chunk c of row i of step r sits at position (r*RS + i)*4 + swz4(i, c),
     // its scale dword at position r*RS + i; positions past the slice re-read
     // valid bytes that are never used
@@ -310,24 +320,36 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 //
 // K advances in 128-wide steps, four to a window.  A step's activation codes
 // (BM x 64 B, chunks swizzled by swz4) and weight codes (BN/16 fragment blocks
-// of 1 KiB, as they are) go global -> LDS by direct loads into one of four
-// stage buffers; the scales of a window (16 B per activation row, 256 B per 16
-// columns) into one of two window buffers.  The four steps of a window are
-// unrolled, so the stage, the scale dword and its byte are constants of the
-// code, and a window's scales are read from LDS once, ahead of the window.
+// of 1 KiB, as they are) go global -> LDS by direct loads into one of STAGES
+// buffers, STAGES - 1 steps ahead; the scales of a window (16 B per activation
+// row, 256 B per 16 columns) into a window buffer, WLEAD windows ahead.  The
+// steps of a window are unrolled, so the stage, the scale dword and its byte
+// are constants of the code, and a window's scales are read from LDS once,
+// under the last MFMAs of the window before.
+//
+// KG > 1: that many groups of WM x WN waves share the tile, each over every
+// KG-th window with buffers of its own, and their partial sums are added
+// through LDS in group order.  A step is a chain (barrier, LDS reads, MFMAs)
+// that one small wave tile per SIMD cannot hide; a second or fourth chain on
+// the same SIMD does, where splitting K over workgroups would send every
+// partial tile through memory.
 //
 // AS16: the activation scale rows are 16-byte aligned and K is a multiple of
 // 512, so a row's window is one 16-byte load (rows of 16 B); otherwise it is
 // four 4-byte loads (planes of BM dwords).  One 4-byte load per row and step
 // touched as many cache lines per step as the codes themselves.
-template <int BM, int BN, int WM, int WN, bool AS16>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool AS16>
 struct TileCfg {
-  static constexpr int kStages = 4;
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kStages = STAGES;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;   // of a group
   static constexpr int kTM = BM / WM / 32, kTN = BN / WN / 32;
   static constexpr int kA = BM * 64, kB = BN * 64, kStage = kA + kB;
   static constexpr int kSB = BN * 16, kSA = BM * 16, kWin = kSB + kSA;
   static constexpr int kWin0 = kStages * kStage;       // the window buffers follow the stages
+  // a window's scales are read a window after they were loaded, or with more
+  // than four stages two windows after: always older by then than the loads
+  // that a step waits for
+  static constexpr int kWLead = STAGES > 4 ? 2 : 1;
   static constexpr int kAIters = kA / (kThreads * 16), kBIters = kB / (kThreads * 16);
   static constexpr int kSBPieces = kSB / 1024, kSAPieces = AS16 ? kSA / 1024 : kSA / 256;
   // loads per stage and per window, the same for every wave: a wave past a
@@ -336,44 +358,47 @@ struct TileCfg {
   static constexpr int kDma = kAIters + kBIters, kWinDma = kSBIters + kSAIters;
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
   static constexpr int kPassN = BN < 128 ? BN : 128;   // columns staged at once by the epilogue
-  static constexpr int kMain = kWin0 + 2 * kWin;
-  static constexpr int kLds = kMain > BM * kPassN * 4 ? kMain : BM * kPassN * 4;
+  static constexpr int kGroup = kWin0 + kWLead * kWin;   // LDS of a group
+  static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
+  static constexpr int kEpi = BM * kPassN * 4;
+  static constexpr int kLds = std::max(KG * kGroup, std::max(kRed, kEpi));
 };
 
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-template <int BM, int BN, int WM, int WN, int OCC, bool GROUPED, bool SPLIT, bool AS16>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int group_m) {
-  using C = TileCfg<BM, BN, WM, WN, AS16>;
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC, bool GROUPED, bool AS16>
+__global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p, int group_m) {
+  using C = TileCfg<BM, BN, WM, WN, KG, STAGES, AS16>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int wg_wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int kg = wg_wave / C::kWaves, wave = wg_wave % C::kWaves;
   const int wm = wave / WN, wn = wave % WN;
   const int N = p.N, KS = p.KS, NT = N >> 4, KQ = (KS + 3) >> 2;
   const int n_tiles = (N + BN - 1) / BN;
-  // K splits cut between windows
-  const int S = SPLIT ? static_cast<int>(gridDim.y) : 1, sp = SPLIT ? static_cast<int>(blockIdx.y) : 0;
-  const int w_begin = SPLIT ? KQ * sp / S : 0, w_end = SPLIT ? KQ * (sp + 1) / S : KQ;
-  const int k_last = min(4 * w_end, KS) - 1;
+  // this group's windows: KG * i + kg for i < n_win
+  const int n_win = (KQ - kg + KG - 1) / KG, n_turns = (KQ + KG - 1) / KG;
+  auto win_of = [&](int i) { return KG * min(i, n_win - 1) + kg; };
 
   int m0, nrows, nt;
-  const uint8_t* w = p.w;
+  const uint8_t *w = p.w, *wsc = p.wsc;
   if constexpr (GROUPED) {
     int e, r1;
     nt = blockIdx.x % n_tiles;
     if (!find_tile<BM>(p.offsets, p.E, p.M, blockIdx.x / n_tiles, e, m0, r1)) return;
     nrows = r1 - m0;
     w += static_cast<size_t>(e) * p.w_stride;
+    wsc += static_cast<size_t>(e) * p.w_stride;
   } else {
     int mt;
     xcd_tile(blockIdx.x, (p.M + BM - 1) / BM, n_tiles, group_m, mt, nt);
     m0 = mt * BM;
     nrows = min(BM, p.M - m0);
   }
-  const uint8_t* wsc = w + p.w_scales;
   const int n0 = nt * BN, nt0 = n0 >> 4;
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+  uint8_t* const glds = lds + kg * C::kGroup;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(glds));
 
   // 32-bit source offsets of the loads (rows past the tile's last and columns
   // past N re-read valid ones; their results are not stored)
@@ -413,9 +438,10 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
       dma16(base + C::kA + ((i - C::kAIters) * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024,
             boff_g[i - C::kAIters]);
   };
-  // the i-th load of window win into its buffer
-  auto win_one = [&](int i, int win) {
-    const uint32_t base = lds0 + C::kWin0 + (win & 1) * C::kWin;
+  // the i-th load of the group's wi-th window into its buffer
+  auto win_one = [&](int i, int wi) {
+    const int win = win_of(wi);
+    const uint32_t base = lds0 + C::kWin0 + (C::kWLead == 2 ? (min(wi, n_win - 1) & 1) * C::kWin : 0);
     if (i < C::kSBIters) {
       dma16(base + ((i * C::kWaves + wave) % C::kSBPieces) * 1024, wsc + static_cast<size_t>(win) * 256, sboff[i]);
     } else {
@@ -455,7 +481,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
   constexpr int kPieces = C::kTN + C::kTM;
   // LDS read piece i of half hh of stage st: weight 0, the activations, the other weights
   auto piece = [&](int st, int hh, Frag& f, int i) {
-    const uint8_t* base = lds + st * C::kStage;
+    const uint8_t* base = glds + st * C::kStage;
     if (i == 0 || i > C::kTM) {
       const int t = i == 0 ? 0 : i - C::kTM;
       f.b[t] = *reinterpret_cast<const v4i*>(base + bbase + t * 2048 + hh * 512);
@@ -463,8 +489,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
       f.a[i - 1] = *reinterpret_cast<const v4i*>(base + abase[hh] + (i - 1) * 2048);
     }
   };
-  auto read_scale = [&](int win, Scale& s, int i) {
-    const uint8_t* base = lds + C::kWin0 + (win & 1) * C::kWin;
+  auto read_scale = [&](int wi, Scale& s, int i) {
+    const uint8_t* base = glds + C::kWin0 + (C::kWLead == 2 ? (min(wi, n_win - 1) & 1) * C::kWin : 0);
     if (i < C::kTN) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) s.b[i][hh] = *reinterpret_cast<const int*>(base + sbbase + i * 512 + hh * 128);
@@ -481,22 +507,18 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
       }
     }
   };
-  auto shift_scale = [&](Scale& s) {
-#pragma unroll
-    for (int t = 0; t < C::kTM; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s.a[t][j] = static_cast<int>(static_cast<uint32_t>(s.a[t][j]) >> sh_a);
-  };
-  // MFMAs of half HH of step J of a window.  Between them: the LDS reads of the
-  // next half (rf, from stage rst, half rhh), this half's share of the loads of
-  // step dks (into stage (J + 3) % 4), of the next window's scale loads (J = 0)
-  // and, in the window's last half, the reads of the next window's scales.
-  auto half = [&](auto jj, auto hh, const Frag& f, const Scale& s, int rst, int rhh, Frag& rf, int dks, int win,
-                  int next_win, Scale& ns) {
-    constexpr int J = decltype(jj)::value, HH = decltype(hh)::value;
+  // Place of a step in the unrolled turn: U is the step's index modulo
+  // lcm(4, STAGES), J = U % 4 its step of the window, U % STAGES its stage.
+  // MFMAs of half HH of a step.  Between them: the LDS reads of the next half
+  // (rf), this half's share of the loads of step dks (STAGES - 1 steps ahead),
+  // and in the step's second half the scale loads of window load_win (J = 0) or
+  // the reads of the next window's scales (J = 3).
+  auto half = [&](auto uu, auto hh, const Frag& f, Frag& rf, const Scale& s, int dks, int load_win, int next_win,
+                  Scale& ns) {
+    constexpr int U = decltype(uu)::value, HH = decltype(hh)::value, J = U % 4;
+    constexpr int kRead = HH == 0 ? U % STAGES : (U + 1) % STAGES;
     constexpr int kN = C::kTN * C::kTM;
     constexpr int d0 = HH * ((C::kDma + 1) / 2), d1 = HH ? C::kDma : (C::kDma + 1) / 2;
-    (void)win;
 #pragma unroll
     for (int n = 0; n < kN || n < kPieces; ++n) {
       if (n < kN) {
@@ -507,14 +529,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
                                                                     s.a[j][J]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (n < kPieces) piece(rst, rhh, rf, n);
+      if (n < kPieces) piece(kRead, 1 - HH, rf, n);
       // the loads, spread evenly over the half's MFMAs
 #pragma unroll
       for (int d = d0; d < d1; ++d)
-        if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, (J + 3) & 3);
+        if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, (U + STAGES - 1) % STAGES);
       if (J == 0 && HH == 1 && n == kN - 1)
 #pragma unroll
-        for (int d = 0; d < C::kWinDma; ++d) win_one(d, next_win);
+        for (int d = 0; d < C::kWinDma; ++d) win_one(d, load_win);
       if (J == 3 && HH == 1) {
 #pragma unroll
         for (int d = 0; d < kPieces; ++d)
@@ -526,80 +548,116 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
 
   // Step s: this wave's loads of step s+1 have landed and its LDS reads are
   // done; barrier (s+1 published, the stage of s-1 free); then the two halves.
-  // The loads of a step are issued three steps ahead.  Steps past the end
-  // re-load the last one (never used).
+  // Steps and windows past the end re-load the last one (never used, or the
+  // same bytes).
   Frag f0, f1;
-  Scale s0, s1;
+  Scale sc, ns;
+  // the ls-th step of this group, in steps of K
+  auto step_of = [&](int ls) { return min(4 * win_of(ls >> 2) + (ls & 3), KS - 1); };
+  if (KG == 1 || n_win > 0) {
 #pragma unroll
-  for (int d = 0; d < C::kWinDma; ++d) win_one(d, w_begin);
+    for (int d = 0; d < C::kWinDma; ++d) win_one(d, 0);
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+    for (int s = 0; s < STAGES - 1; ++s) {
 #pragma unroll
-    for (int i = 0; i < C::kDma; ++i) dma_one(i, min(4 * w_begin + s, k_last), s);
-  wait_vm<2 * C::kDma>();
+      for (int i = 0; i < C::kDma; ++i) dma_one(i, step_of(s), s);
+      // (with two windows of lead, the second is issued where step -4 would have)
+      if (C::kWLead == 2 && s == STAGES - 5)
+#pragma unroll
+        for (int d = 0; d < C::kWinDma; ++d) win_one(d, 1);
+    }
+  }
+  // newer than the first window and step 0: the other steps, and the second window
+  wait_vm<(STAGES - 2) * C::kDma + (C::kWLead == 2 ? C::kWinDma : 0)>();
   __syncthreads();
+  if (KG == 1 || n_win > 0) {
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) piece(0, 0, f0, i);
+    for (int i = 0; i < kPieces; ++i) piece(0, 0, f0, i);
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) read_scale(w_begin, s0, i);
-  auto step = [&](auto jj, int win, Scale& s, Scale& ns) {
-    constexpr int J = decltype(jj)::value;
-    const int ks = 4 * win + J, next = min(win + 1, w_end - 1);
-    // newer loads that may be outstanding: those of step s+2, and the window's
-    // scale loads when they were issued after them (in step 0)
-    wait_vm<C::kDma + (J == 1 ? C::kWinDma : 0)>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int i = 0; i < kPieces; ++i) read_scale(0, ns, i);
+  }
+  // step J of the group's wi-th window (live: it exists)
+  auto step = [&](auto uu, int wi, bool live) {
+    constexpr int U = decltype(uu)::value, J = U % 4;
+    if (KG == 1 || live) {
+      // loads newer than step s+1's: STAGES - 3 steps, and the scale loads that
+      // the second halves of steps s-d (J = 0) issued, where they are newer
+      constexpr int kScaleEvents = (J >= 1 && J <= STAGES - 2 ? 1 : 0) + (J + 4 <= STAGES - 2 ? 1 : 0);
+      wait_vm<(STAGES - 3) * C::kDma + kScaleEvents * C::kWinDma>();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (J == 0) shift_scale(s);
-    half(jj, Int<0>{}, f0, s, J, 1, f1, min(ks + 3, k_last), win, next, ns);
-    half(jj, Int<1>{}, f1, s, (J + 1) & 3, 0, f0, min(ks + 3, k_last), win, next, ns);
+    if (KG > 1 && !live) return;
+    if constexpr (J == 0) {
+#pragma unroll
+      for (int t = 0; t < C::kTM; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc.a[t][j] = static_cast<int>(static_cast<uint32_t>(ns.a[t][j]) >> sh_a);
+#pragma unroll
+      for (int t = 0; t < C::kTN; ++t)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) sc.b[t][hh] = ns.b[t][hh];
+    }
+    const int dks = step_of(4 * wi + J + STAGES - 1);
+    half(uu, Int<0>{}, f0, f1, sc, dks, wi + C::kWLead, wi + 1, ns);
+    half(uu, Int<1>{}, f1, f0, sc, dks, wi + C::kWLead, wi + 1, ns);
   };
-  // two windows per turn, so the scale sets swap without copies
-  auto window = [&](int win, Scale& s, Scale& ns) {
-    step(Int<0>{}, win, s, ns);
-    if (4 * win + 1 <= k_last) step(Int<1>{}, win, s, ns);
-    if (4 * win + 2 <= k_last) step(Int<2>{}, win, s, ns);
-    if (4 * win + 3 <= k_last) step(Int<3>{}, win, s, ns);
+  // (with one group, steps past the end are skipped; several groups meet at
+  // every barrier, so those run it empty)
+  auto window = [&](auto ww, int wi) {
+    constexpr int W = 4 * decltype(ww)::value;
+    if (wi >= n_turns) return;
+    const int k0 = 4 * (KG * wi + kg);
+    const bool here = wi < n_win;
+    step(Int<W>{}, wi, here);
+    if (KG > 1 || k0 + 1 < KS) step(Int<W + 1>{}, wi, here && k0 + 1 < KS);
+    if (KG > 1 || k0 + 2 < KS) step(Int<W + 2>{}, wi, here && k0 + 2 < KS);
+    if (KG > 1 || k0 + 3 < KS) step(Int<W + 3>{}, wi, here && k0 + 3 < KS);
   };
-  for (int win = w_begin; win < w_end; win += 2) {
-    window(win, s0, s1);
-    if (win + 1 < w_end) window(win + 1, s1, s0);
+  constexpr int kTurn = STAGES % 4 == 0 ? STAGES / 4 : (STAGES % 2 == 0 ? STAGES / 2 : STAGES);  // windows
+  static_assert(STAGES >= 3 && kTurn <= 3, "windows unrolled below");
+  for (int wi = 0; wi < n_turns; wi += kTurn) {
+    window(Int<0>{}, wi);
+    if constexpr (kTurn > 1) window(Int<1>{}, wi + 1);
+    if constexpr (kTurn > 2) window(Int<2>{}, wi + 2);
   }
   wait_vm<0>();
 
-  // K splits: partial tile in fragment order through the workspace
-  if constexpr (SPLIT) {
-    if (S > 1) {
-      __shared__ int last;
-      constexpr int kNV = C::kTN * C::kTM * 16;
-      float* base = p.slab + (static_cast<size_t>(blockIdx.x) * C::kWaves + wave) * (kNV * 64) + l;
-      const size_t stride = static_cast<size_t>(gridDim.x) * C::kWaves * (kNV * 64);
+  // the groups' partial sums, added by group 0 in group order.  Fragment order:
+  // element r of lane l of sub-tile (i, j) at quarter r/4, 16 bytes a lane.
+  if constexpr (KG > 1) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    constexpr int kWaveBytes = C::kTN * C::kTM * 4096;
+    if (kg > 0) {
+      uint8_t* dst = lds + ((kg - 1) * C::kWaves + wave) * kWaveBytes + l * 16;
 #pragma unroll
       for (int i = 0; i < C::kTN; ++i)
 #pragma unroll
         for (int j = 0; j < C::kTM; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            __hip_atomic_store(base + sp * stride + ((i * C::kTM + j) * 16 + r) * 64, acc[i][j][r], __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0);
-      asm volatile("" ::: "memory");
-      __syncthreads();
-      if (tid == 0)
-        last = __hip_atomic_fetch_add(&p.counters[blockIdx.x], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == S - 1;
-      __syncthreads();
-      if (!last) return;
-      float sum[kNV];
-      sum_partials<kNV, 64, 1>(sum, base, stride, S);
+          for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<float4*>(dst + (i * C::kTM + j) * 4096 + r * 1024) = make_float4(
+                acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
+    }
+    __syncthreads();
+    if (kg == 0) {
 #pragma unroll
-      for (int i = 0; i < C::kTN; ++i)
+      for (int g = 1; g < KG; ++g)
 #pragma unroll
-        for (int j = 0; j < C::kTM; ++j)
+        for (int i = 0; i < C::kTN; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] = sum[(i * C::kTM + j) * 16 + r];
-      if (tid == 0) __hip_atomic_store(&p.counters[blockIdx.x], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          for (int j = 0; j < C::kTM; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float4 v = *reinterpret_cast<const float4*>(
+                  lds + ((g - 1) * C::kWaves + wave) * kWaveBytes + l * 16 + (i * C::kTM + j) * 4096 + r * 1024);
+              acc[i][j][4 * r] += v.x;
+              acc[i][j][4 * r + 1] += v.y;
+              acc[i][j][4 * r + 2] += v.z;
+              acc[i][j][4 * r + 3] += v.w;
+            }
     }
   }
 
@@ -611,13 +669,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
   constexpr int kW = kPP * 32;                      // a wave's columns per pass
   static_assert(WN * kW == kPassN && C::kTN % kPasses == 0, "");
   constexpr int kLanes = kPassN / 8;                // lanes per row, 8 columns each
-  constexpr int kRows = C::kThreads / kLanes;
+  constexpr int kRows = C::kThreads * KG / kLanes;
   static_assert(BM % kRows == 0, "");
   const int lane8 = tid % kLanes, rsub = tid / kLanes;
 #pragma unroll
   for (int h = 0; h < kPasses; ++h) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();
+    if (kg == 0)   // (the other groups have handed their sums over)
 #pragma unroll
     for (int j = 0; j < C::kTM; ++j) {
       uint8_t* rowp = lds + arow[j] * (kPassN * 4);
@@ -652,8 +711,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_w4a4_tile(W4A4Args p, int
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kStreamMaxM = 64;   // dense: up to here the weight stream runs
 constexpr size_t kMaxStreamLds = 160 * 1024 - 256;
+
+// The weight stream takes up to 16 rows, and up to 64 where K is long and N
+// narrow (K >= 12288, N < 8192): there its K splits over workgroups keep more
+// of the GPU loading than the tiles' K groups (M = 48 N = 5120 K = 17408 23.8
+// us against 29.3, but N = 10240 38.3 against 31.4, and N = K = 5120 11.0
+// against 8.5).
+bool use_stream(int M, int N, int KS) { return M <= 16 || (M <= 64 && KS >= 96 && N < 8192); }
 
 struct StreamCfg {
   int mb, tw, kw, t, r, rs, groups, mtiles, s, iters;
@@ -665,37 +730,29 @@ size_t stream_lds(const StreamCfg& d) {
   return std::max(slice, red);
 }
 
+// Swept at 1 to 16 rows over K = 512 .. 17408, N = 512 .. 34816, weights pooled
+// past the last-level cache: a workgroup covers all of a short K with no idle
+// K-wave, a longer one in runs of 40 steps (24 from K = 12288 on with wide N).
+// With M = 8: K = 1024 N = 17408 6.95 us with ten K-waves, 4.4 with two; K =
+// 5120 N = 5120 5.8 -> 5.4; K = 5120 N = 17408 10.9, K = 17408 N = 5120 12.1.
 StreamCfg dense_stream_cfg(int M, int N, int KS) {
   StreamCfg d{};
   d.mb = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
   d.rs = std::min(M, 16 * d.mb);
   d.mtiles = (M + 16 * d.mb - 1) / (16 * d.mb);
+  const int nt = N / 16;
   auto set = [&](int tw, int kw, int t, int r) { d.tw = tw; d.kw = kw; d.t = t; d.r = r; };
-  if (d.mb == 1) {
-    if (KS >= 96) set(4, 3, 1, 8);
-    else if (M >= 5 && N / 16 >= 640) set(3, 5, 1, 8);
-    else set(1, 10, 1, 4);
-  } else {
-    set(8, 1, 1, 8);
-  }
-  d.groups = (N / 16 + d.tw * d.t - 1) / (d.tw * d.t);
+  if (d.mb > 1) set(8, 1, 1, 8);
+  else if (KS <= 4) set(8, 1, 1, 4);
+  else if (KS <= 8) set(4, 2, 1, 4);
+  else if (KS <= 16) set(2, 4, 1, 4);
+  else if (nt < 256) set(1, 10, 1, 4);
+  else if (KS >= 96) set(4, 3, 1, 8);
+  else if (nt < 512) set(2, 5, 1, 8);
+  else set(3, 5, 1, 8);
+  d.groups = (nt + d.tw * d.t - 1) / (d.tw * d.t);
   d.s = (KS + d.kw * d.r - 1) / (d.kw * d.r);
   d.iters = 1;
-  return d;
-}
-
-StreamCfg grouped_stream_cfg(int S, int E, int N, int KS, int mb) {
-  StreamCfg d{};
-  d.mb = mb;
-  d.rs = 16 * mb;
-  d.mtiles = tile_bound(S, E, 16 * mb);
-  d.tw = mb == 1 ? 2 : 4;
-  d.kw = mb == 1 ? 4 : 2;
-  d.t = 1;
-  d.r = 4;
-  d.groups = (N / 16 + d.tw * d.t - 1) / (d.tw * d.t);
-  d.s = 1;
-  d.iters = (KS + d.kw * d.r - 1) / (d.kw * d.r);
   return d;
 }
 
@@ -721,56 +778,106 @@ int run_dense_stream(W4A4Args& p, void* ws, hipStream_t st) {
     p.counters = static_cast<int*>(ws);
     p.slab = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
   }
-  if (d.mb == 1 && d.kw == 3) return launch_stream<1, 4, 3, 1, 8, false>(d, p, st);
-  if (d.mb == 1 && d.kw == 5) return launch_stream<1, 3, 5, 1, 8, false>(d, p, st);
-  if (d.mb == 1) return launch_stream<1, 1, 10, 1, 4, false>(d, p, st);
+  // one instantiation per configuration of dense_stream_cfg
+  if (d.mb == 4) return launch_stream<4, 8, 1, 1, 8, false>(d, p, st);
   if (d.mb == 2) return launch_stream<2, 8, 1, 1, 8, false>(d, p, st);
-  return launch_stream<4, 8, 1, 1, 8, false>(d, p, st);
-}
-
-// Tiles of the dense problem: 256x256 where they fill the GPU (one workgroup
-// per CU), otherwise 128x128 with K split until about 256 workgroups run.
-struct TilePlan {
-  bool large;
-  int tiles, s;
-};
-TilePlan tile_plan(int M, int N, int KS) {
-  const int big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 192) return TilePlan{true, big, 1};
-  const int t = ((M + 127) / 128) * ((N + 127) / 128);
-  const int s = t < 256 ? std::max(1, std::min(256 / t, KS / 8)) : 1;
-  return TilePlan{false, t, s};
+  if (d.tw == 8) return launch_stream<1, 8, 1, 1, 4, false>(d, p, st);
+  if (d.kw == 2) return launch_stream<1, 4, 2, 1, 4, false>(d, p, st);
+  if (d.kw == 4) return launch_stream<1, 2, 4, 1, 4, false>(d, p, st);
+  if (d.kw == 10) return launch_stream<1, 1, 10, 1, 4, false>(d, p, st);
+  if (d.kw == 3) return launch_stream<1, 4, 3, 1, 8, false>(d, p, st);
+  if (d.tw == 2) return launch_stream<1, 2, 5, 1, 8, false>(d, p, st);
+  return launch_stream<1, 3, 5, 1, 8, false>(d, p, st);
 }
 
 // One 16-byte load per row and window of activation scales (see TileCfg).
 bool scales16(const W4A4Args& p) { return p.KS % 4 == 0 && p.lds % 16 == 0 && bs_aligned(p.as, 16); }
 
-int run_dense_tile(W4A4Args& p, void* ws, hipStream_t st) {
-  const TilePlan pl = tile_plan(p.M, p.N, p.KS);
-  const bool as16 = scales16(p);
-  if (pl.large) {
-    if (as16) k_w4a4_tile<256, 256, 2, 2, 1, false, false, true><<<dim3(pl.tiles, 1), 256, 0, st>>>(p, 4);
-    else k_w4a4_tile<256, 256, 2, 2, 1, false, false, false><<<dim3(pl.tiles, 1), 256, 0, st>>>(p, 4);
-    return bs_launch_status();
-  }
-  if (pl.s > 1) {
-    p.counters = static_cast<int*>(ws);
-    p.slab = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
-  }
-  if (as16) k_w4a4_tile<128, 128, 2, 2, 2, false, true, true><<<dim3(pl.tiles, pl.s), 256, 0, st>>>(p, 4);
-  else k_w4a4_tile<128, 128, 2, 2, 2, false, true, false><<<dim3(pl.tiles, pl.s), 256, 0, st>>>(p, 4);
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC, bool GROUPED>
+int launch_tile(const W4A4Args& p, int64_t wgs, hipStream_t st) {
+  if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
+  const dim3 grid(static_cast<uint32_t>(wgs)), block(64 * WM * WN * KG);
+  // group_m 4: the raster's m-tiles that sweep n together (2 to 16 within 1%)
+  if (scales16(p)) k_w4a4_tile<BM, BN, WM, WN, KG, STAGES, OCC, GROUPED, true><<<grid, block, 0, st>>>(p, 4);
+  else k_w4a4_tile<BM, BN, WM, WN, KG, STAGES, OCC, GROUPED, false><<<grid, block, 0, st>>>(p, 4);
   return bs_launch_status();
+}
+
+// The dense tile shapes and what a launch of each takes, in us: with x = tiles
+// / 256 (one per CU) and R = ceil(x) rounds,
+//   t = start + R * (round + steps * step) + x * steps * load
+// least squares over 14 row counts from 32 to 4096, N = 512 .. 17408 and
+// K = 512 .. 17408 (rms 5 to 9%; the shape with the smallest t is the measured
+// best or within 1% of it, at worst 13%).
+struct TileShape {
+  int bm, bn;
+  float start, round, step, load;
+};
+constexpr TileShape kTiles[] = {
+    {256, 256, 0.0f, 7.93f, 0.453f, 0.356f},  // 4 waves of 128 x 128
+    {128, 128, 2.35f, 1.19f, 0.171f, 0.146f}, // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 1.44f, 2.25f, 0.118f, 0.092f},  // 2 K groups of 4 waves of 64 x 32
+    {64, 64, 2.47f, 0.83f, 0.075f, 0.055f},   // 2 K groups of 2 waves of 64 x 32, two workgroups a CU
+    {64, 64, 1.62f, 2.32f, 0.066f, 0.079f},   // 4 K groups of the same
+};
+float tile_cost(int i, int M, int N, int KS) {
+  const TileShape& t = kTiles[i];
+  const int64_t tiles = static_cast<int64_t>((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+  const float x = static_cast<float>(tiles) / 256.0f;
+  return t.start + std::ceil(x) * (t.round + KS * t.step) + x * KS * t.load;
+}
+int best_tile(int M, int N, int KS) {
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (tile_cost(i, M, N, KS) < tile_cost(best, M, N, KS)) best = i;
+  return best;
+}
+
+// columns [n0, n1) of the problem as tiles of shape i
+int run_tiles(int i, const W4A4Args& q, int n0, int n1, hipStream_t st) {
+  W4A4Args p = q;
+  const size_t nt = static_cast<size_t>(n0) / 16;
+  p.w += nt * p.KS * 1024;
+  p.wsc += nt * ((p.KS + 3) / 4) * 256;
+  p.c += n0;
+  p.N = n1 - n0;
+  const int64_t wgs =
+      static_cast<int64_t>((p.M + kTiles[i].bm - 1) / kTiles[i].bm) * ((p.N + kTiles[i].bn - 1) / kTiles[i].bn);
+  switch (i) {
+    case 0: return launch_tile<256, 256, 2, 2, 1, 4, 1, false>(p, wgs, st);
+    case 1: return launch_tile<128, 128, 2, 2, 1, 4, 2, false>(p, wgs, st);
+    case 2: return launch_tile<64, 128, 1, 4, 2, 4, 2, false>(p, wgs, st);
+    case 3: return launch_tile<64, 64, 1, 2, 2, 4, 2, false>(p, wgs, st);
+    default: return launch_tile<64, 64, 1, 2, 4, 4, 2, false>(p, wgs, st);
+  }
+}
+
+// One shape for all columns; or, where the large tiles would end in a partial
+// round, large tiles over as many columns as whole rounds take and the rest as
+// the shape that is quickest there (the second launch costs about 1 us more).
+int run_dense_tile(const W4A4Args& p, hipStream_t st) {
+  const int b = best_tile(p.M, p.N, p.KS);
+  const int mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
+  const int rounds = mt * static_cast<int64_t>(nt) / 256;
+  if (rounds >= 1) {
+    const int n1 = rounds * 256 / mt * 256;   // < N unless the rounds are whole
+    if (n1 > 0 && n1 < p.N) {
+      const int r = best_tile(p.M, p.N - n1, p.KS);
+      if (tile_cost(0, p.M, n1, p.KS) + tile_cost(r, p.M, p.N - n1, p.KS) + 1.0f < tile_cost(b, p.M, p.N, p.KS)) {
+        const int rc = run_tiles(0, p, 0, n1, st);
+        return rc != BS_OK ? rc : run_tiles(r, p, n1, p.N, st);
+      }
+    }
+  }
+  return run_tiles(b, p, 0, p.N, st);
 }
 
 }  // namespace
 
 size_t bs_w4a4_workspace(int M, int N, int K) {
-  if (M <= kStreamMaxM) {
-    const StreamCfg d = dense_stream_cfg(M, N, K / 128);
-    return d.s > 1 ? kWsCounterBytes + static_cast<size_t>(d.s) * d.mtiles * d.groups * d.tw * d.t * d.mb * 1024 : 0;
-  }
-  const TilePlan pl = tile_plan(M, N, K / 128);
-  return pl.s > 1 ? kWsCounterBytes + static_cast<size_t>(pl.s) * pl.tiles * 128 * 128 * sizeof(float) : 0;
+  if (!use_stream(M, N, K / 128)) return 0;
+  const StreamCfg d = dense_stream_cfg(M, N, K / 128);
+  return d.s > 1 ? kWsCounterBytes + static_cast<size_t>(d.s) * d.mtiles * d.groups * d.tw * d.t * d.mb * 1024 : 0;
 }
 
 int bs_launch_w4a4(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const uint8_t* w, size_t w_scales,
@@ -781,15 +888,25 @@ int bs_launch_w4a4(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds
   p.lda = static_cast<uint32_t>(lda);
   p.lds = static_cast<uint32_t>(lds);
   p.w = w;
-  p.w_scales = w_scales;
+  p.wsc = w + w_scales;
   p.c = c;
   p.ldc = ldc;
   p.M = M;
   p.N = N;
   p.KS = K / 128;
-  return M <= kStreamMaxM ? run_dense_stream(p, ws, st) : run_dense_tile(p, ws, st);
+  return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, st);
 }
 
+// Row tiles by S / E, the rows an expert would have if they were spread evenly
+// (swept at 256, 64 and 16 experts, S / E from 1/32 to 4096):
+//   - short K and few rows: the weight stream, whose workgroup covers 256
+//     columns (256 experts N = 2048 K = 512: S / E = 2 22 us against 27 with the
+//     tiles below, 8 28 against 31);
+//   - up to 48 rows: 64 x 128 tiles, three workgroups a CU, whose loads run
+//     ahead over all of K (256 experts N = 1024 K = 2048: S / E = 2 40 us, the
+//     stream 42 to 45; 32 33 us, the tiles below 40);
+//   - above: 128 x 256 tiles, two workgroups a CU, so one's stores run under the
+//     other's MFMAs (S / E = 256 111 us; 128 x 128 131, 256 x 256 150).
 int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const int* offsets,
                            const int* rows, const uint8_t* w, size_t w_scales, size_t w_stride, uint16_t* c,
                            int64_t ldc, int S, int Ma, int E, int N, int K, hipStream_t st) {
@@ -799,7 +916,7 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
   p.lda = static_cast<uint32_t>(lda);
   p.lds = static_cast<uint32_t>(lds);
   p.w = w;
-  p.w_scales = w_scales;
+  p.wsc = w + w_scales;
   p.w_stride = w_stride;
   p.c = c;
   p.ldc = ldc;
@@ -810,14 +927,14 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
   p.rows = rows;
   p.E = E;
   p.Ma = Ma;
-  const int avg = S / E;   // rows per expert if they were spread evenly
-  if (avg <= 16) return launch_stream<1, 2, 4, 1, 4, true>(grouped_stream_cfg(S, E, N, p.KS, 1), p, st);
-  if (avg <= 48) return launch_stream<4, 4, 2, 1, 4, true>(grouped_stream_cfg(S, E, N, p.KS, 4), p, st);
-  const int64_t wgs = static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 127) / 128);
-  if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
-  if (scales16(p))
-    k_w4a4_tile<128, 128, 2, 2, 2, true, false, true><<<dim3(static_cast<uint32_t>(wgs)), 256, 0, st>>>(p, 0);
-  else
-    k_w4a4_tile<128, 128, 2, 2, 2, true, false, false><<<dim3(static_cast<uint32_t>(wgs)), 256, 0, st>>>(p, 0);
-  return bs_launch_status();
+  const int avg = S / E;
+  if (p.KS <= 8 && avg < 16) {
+    StreamCfg d{1, 8, 1, 2, 4, 16, (N / 16 + 15) / 16, tile_bound(S, E, 16), 1, (p.KS + 3) / 4};
+    return launch_stream<1, 8, 1, 2, 4, true>(d, p, st);
+  }
+  if (avg <= 48)
+    return launch_tile<64, 128, 1, 4, 1, 4, 3, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 127) / 128),
+                                                     st);
+  return launch_tile<128, 256, 2, 2, 1, 3, 2, true>(p, static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 255) / 256),
+                                                    st);
 }
