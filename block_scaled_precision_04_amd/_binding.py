@@ -174,11 +174,16 @@ def _on_device(fn, *ts):
 
 
 def _on_current(fn, *ts):
-    """Every tensor lives on the current GPU: the launch goes to its current stream."""
-    dev = _on_device(fn, *ts)
+    """Every tensor lives on the current GPU: the launch goes to its current
+    stream, whose handle is returned."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            _on_device(fn, *ts)
     cur = torch.cuda.current_device()
-    if dev.index != cur:
-        _need(False, fn, f"tensors are on {dev}, the current device is cuda:{cur}")
+    if dev != cur:
+        _need(False, fn, f"tensors are on cuda:{dev}, the current device is cuda:{cur}")
+    return _raw_stream(cur) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def _row_stride(t):
@@ -251,13 +256,13 @@ def prelayout_mxfp4_experts(w_packed, w_e8m0):
     nbytes = lib().bs_prelayout_mxfp4_bytes(N, K)
     if nbytes == 0:
         raise BsError("bs_prelayout_mxfp4_bytes", -2)
-    _on_current(fn, w_packed, w_e8m0)
+    stream = _on_current(fn, w_packed, w_e8m0)
     out = torch.empty((E, nbytes), dtype=torch.uint8, device=w_packed.device)
     desc = WDesc()
     for e in range(E):
         wp, sc = w_packed[e].contiguous(), w_e8m0[e].contiguous()
         _check(fn, lib().bs_prelayout_mxfp4(_ptr(wp), _ptr(sc), _ptr(out[e]), nbytes, N, K, ctypes.byref(desc),
-                                            _stream()))
+                                            stream))
     return out, desc
 
 
@@ -386,11 +391,11 @@ def bsgemm_w4a4_mxfp4(a, a_scale, desc, w_pre, out=None, ws=None):
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     else:
         _arg(fn, "out", out, (M, N), _BF16)
-    _on_current(fn, a, a_scale, w_pre, out, ws)
+    stream = _on_current(fn, a, a_scale, w_pre, out, ws)
     ws_p, ws_n = _ws(fn, ws)
     _check(fn, lib().bsgemm_w4a4_mxfp4(
         _ptr(a), _row_stride(a), _ptr(a_scale), _row_stride(a_scale), ctypes.byref(desc), _ptr(w_pre), _ptr(out),
-        _row_stride(out), M, N, K, ws_p, ws_n, _stream()))
+        _row_stride(out), M, N, K, ws_p, ws_n, stream))
     return out
 
 
@@ -418,10 +423,10 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
         out = torch.empty((S, N), dtype=torch.bfloat16, device=a.device)
     else:
         _arg(fn, "out", out, (S, N), _BF16)
-    _on_current(fn, a, a_scale, offsets, w_pre, rows, out)
+    stream = _on_current(fn, a, a_scale, offsets, w_pre, rows, out)
     _check(fn, lib().bsgemm_w4a4_mxfp4_grouped(
         _ptr(a), _row_stride(a), _ptr(a_scale), _row_stride(a_scale), Ma, _ptr(offsets), _ptr(rows),
-        ctypes.byref(desc), _ptr(w_pre), _row_stride(w_pre), _ptr(out), _row_stride(out), S, E, N, K, _stream()))
+        ctypes.byref(desc), _ptr(w_pre), _row_stride(w_pre), _ptr(out), _row_stride(out), S, E, N, K, stream))
     return out
 
 
@@ -598,10 +603,10 @@ def quant_mxfp4(x, q=None, scale=None):
         _need(False, fn, f"K = {K} must be a multiple of 32")
     _arg(fn, "x", x, (M, K), _BF16, unit_inner=False)
     q, scale = _mxfp4_out(fn, q, scale, M, K, x.device)
-    _on_current(fn, x, q, scale)
+    stream = _on_current(fn, x, q, scale)
     if x.stride(1) != 1 or (M > 1 and (x.stride(0) < K or x.stride(0) % 8)) or x.data_ptr() % 16:
         x = x.clone(memory_format=torch.contiguous_format)
-    _check(fn, lib().quant_mxfp4(_ptr(x), _row_stride(x), _ptr(q), _ptr(scale), M, K, _stream()))
+    _check(fn, lib().quant_mxfp4(_ptr(x), _row_stride(x), _ptr(q), _ptr(scale), M, K, stream))
     return q, scale
 
 
@@ -619,9 +624,9 @@ def silu_mul_quant_mxfp4(gu, q=None, scale=None, rows=None):
     if rows is not None:
         _arg(fn, "rows", rows, (1,), _I32)
     q, scale = _mxfp4_out(fn, q, scale, M, N, gu.device)
-    _on_current(fn, gu, q, scale, rows)
+    stream = _on_current(fn, gu, q, scale, rows)
     gu = gu.contiguous()
-    _check(fn, lib().silu_mul_quant_mxfp4(_ptr(gu), _ptr(q), _ptr(scale), _ptr(rows), M, N, _stream()))
+    _check(fn, lib().silu_mul_quant_mxfp4(_ptr(gu), _ptr(q), _ptr(scale), _ptr(rows), M, N, stream))
     return q, scale
 
 
@@ -638,9 +643,9 @@ def dequant_mxfp4(q, scale, out=None):
         out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
     else:
         _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
-    _on_current(fn, q, scale, out)
+    stream = _on_current(fn, q, scale, out)
     q, scale = q.contiguous(), scale.contiguous()
-    _check(fn, lib().dequant_mxfp4(_ptr(q), _ptr(scale), _ptr(out), M, K, _stream()))
+    _check(fn, lib().dequant_mxfp4(_ptr(q), _ptr(scale), _ptr(out), M, K, stream))
     return out
 
 
@@ -667,10 +672,10 @@ def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
         offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
     else:
         _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
-    _on_current(fn, ids, rows, pos, offsets, ws)
+    stream = _on_current(fn, ids, rows, pos, offsets, ws)
     ids = ids.contiguous()
     ws_p, ws_n = _ws(fn, ws)
-    _check(fn, lib().moe_sort(_ptr(ids), _ptr(rows), _ptr(pos), _ptr(offsets), T, k, E, ws_p, ws_n, _stream()))
+    _check(fn, lib().moe_sort(_ptr(ids), _ptr(rows), _ptr(pos), _ptr(offsets), T, k, E, ws_p, ws_n, stream))
     return rows, pos, offsets
 
 
@@ -692,9 +697,9 @@ def moe_gather(x, pos, out=None):
         out = torch.empty((T * k, K), dtype=torch.bfloat16, device=x.device)
     else:
         _arg(fn, "out", out, (T * k, K), _BF16, contiguous=True)
-    _on_current(fn, x, pos, out)
+    stream = _on_current(fn, x, pos, out)
     x = x.contiguous()
-    _check(fn, lib().moe_gather(_ptr(x), _ptr(pos), _ptr(out), T, k, K, _stream()))
+    _check(fn, lib().moe_gather(_ptr(x), _ptr(pos), _ptr(out), T, k, K, stream))
     return out
 
 
@@ -712,9 +717,9 @@ def moe_combine(y, pos, weights=None, out=None):
         out = torch.empty((T, K), dtype=torch.bfloat16, device=y.device)
     else:
         _arg(fn, "out", out, (T, K), _BF16, contiguous=True)
-    _on_current(fn, y, pos, weights, out)
+    stream = _on_current(fn, y, pos, weights, out)
     y = y.contiguous()
-    _check(fn, lib().moe_combine(_ptr(y), _ptr(pos), _ptr(weights), _ptr(out), T, k, K, _stream()))
+    _check(fn, lib().moe_combine(_ptr(y), _ptr(pos), _ptr(weights), _ptr(out), T, k, K, stream))
     return out
 
 
@@ -736,8 +741,8 @@ def moe_combine_backward(dout, y, pos, weights, dy=None, dweights=None):
         dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
     else:
         _arg(fn, "dweights", dweights, (T, k), _F32, contiguous=True)
-    _on_current(fn, dout, y, pos, weights, dy, dweights)
+    stream = _on_current(fn, dout, y, pos, weights, dy, dweights)
     dout, y = dout.contiguous(), y.contiguous()
     _check(fn, lib().moe_combine_backward(_ptr(dout), _ptr(y), _ptr(pos), _ptr(weights), _ptr(dy), _ptr(dweights),
-                                          T, k, K, _stream()))
+                                          T, k, K, stream))
     return dy, dweights
