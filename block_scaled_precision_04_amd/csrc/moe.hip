@@ -16,11 +16,16 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxExperts = 1024;
-constexpr int kOneBlockPairs = 8192;   // up to here one workgroup sorts the batch
-constexpr int kBlockPairs = 4096;      // pairs of a workgroup beyond that
-constexpr int kMaxBlocks = 256;
+// Up to kOneBlockPairs one workgroup sorts the batch (E = 256: 3.6 us at 64
+// pairs, 8.0 at 4096, 12.5 at 8192, where two launches of four workgroups take
+// 8.6).  Beyond that a workgroup takes kBlockPairs, or as many as leave
+// kMaxBlocks workgroups, since each of them reads all the others' counts
+// (65536 pairs: 1024 a workgroup 9.3 us, 2048 9.5, 4096 11.4; 262144: 15.1,
+// 12.4, 13.1).
+constexpr int kOneBlockPairs = 4096;
+constexpr int kBlockPairs = 2048;
+constexpr int kMaxBlocks = 128;
 
-// Pairs per workgroup: kBlockPairs until that takes kMaxBlocks workgroups.
 int sort_chunk(int P) {
   if (P <= kOneBlockPairs) return P;
   return std::max(kBlockPairs, ((P + kMaxBlocks - 1) / kMaxBlocks + 1023) / 1024 * 1024);
@@ -67,7 +72,7 @@ BS_INLINE void wave_lds_fence() {
 // (from hist where there are several workgroups, whose counts all of them add
 // up), then every wave places its pairs 64 at a time: a lane's rank among the
 // lanes of its expert comes from one ballot per id bit.
-// Dynamic LDS: counts [waves][E], totals [E].
+// Dynamic LDS: counts [waves][E], totals [E], counts of earlier workgroups [E].
 __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict__ ids, const int* __restrict__ hist,
                                                            int* __restrict__ rows, int* __restrict__ pos,
                                                            int* __restrict__ offsets, int P, int k, int E, int chunk,
@@ -76,31 +81,48 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict
   const int waves = blockDim.x >> 6;
   int* cnt = lds;                // [waves][E]: counts, then the wave's next slot
   int* tot = lds + waves * E;    // [E]: pairs of the expert, then its start
+  int* pre = tot + E;            // [E]: of those, in earlier workgroups
   __shared__ int kept_total;
   const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-  for (int i = threadIdx.x; i < waves * E; i += blockDim.x) cnt[i] = 0;
+  for (int i = threadIdx.x; i < (waves + 2) * E; i += blockDim.x) cnt[i] = 0;
   __syncthreads();
   const Run r = wave_run(P, chunk, wave, waves);
   for (int p = r.begin + l; p < r.end; p += 64) {
     const int id = ids[p];
     if (id >= 0 && id < E) atomicAdd(&cnt[wave * E + id], 1);
   }
+  if (hist != nullptr) {
+    // the workgroups' counts, `parts` threads to an expert, four loads at once
+    // (one thread per expert, a load at a time, took half the kernel)
+    const int nb = gridDim.x, me = blockIdx.x, parts = max(1, static_cast<int>(blockDim.x) / E);
+    for (int i = threadIdx.x; i < E * parts; i += blockDim.x) {
+      const int e = i % E;
+      int all = 0, run = 0;
+      for (int b0 = i / E; b0 < nb; b0 += 4 * parts) {
+        int c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) c[u] = hist[static_cast<size_t>(min(b0 + u * parts, nb - 1)) * E + e];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int b = b0 + u * parts;
+          all += b < nb ? c[u] : 0;
+          run += b < me ? c[u] : 0;
+        }
+      }
+      atomicAdd(&tot[e], all);
+      atomicAdd(&pre[e], run);
+    }
+  }
   __syncthreads();
   // cnt[w][e] := pairs of e in earlier workgroups and earlier waves of this one
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int all = 0, run = 0;
-    if (hist != nullptr)
-      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-        const int c = hist[static_cast<size_t>(b) * E + e];
-        all += c;
-        run += b < static_cast<int>(blockIdx.x) ? c : 0;
-      }
+    int run = pre[e];
     for (int w = 0; w < waves; ++w) {
       const int c = cnt[w * E + e];
       cnt[w * E + e] = run;
       run += c;
     }
-    tot[e] = hist != nullptr ? all : run;
+    if (hist == nullptr) tot[e] = run;
   }
   __syncthreads();
   if (wave == 0) {   // exclusive scan of tot: each lane a run of experts
@@ -129,9 +151,10 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict
     }
   }
   __syncthreads();
+  int next = r.begin + l < r.end ? ids[r.begin + l] : -1;
   for (int p0 = r.begin; p0 < r.end; p0 += 64) {
-    const int p = p0 + l;
-    const int id = p < r.end ? ids[p] : -1;
+    const int p = p0 + l, id = next;
+    next = p + 64 < r.end ? ids[p + 64] : -1;   // loaded under this round's ballots
     const bool keep = id >= 0 && id < E;
     unsigned long long same = __ballot(keep);
     for (int b = 0; b < id_bits; ++b) {
@@ -322,15 +345,16 @@ BS_API int moe_sort(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* of
     hist = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
     k_moe_count<<<nb, kSortThreads, 0, st>>>(ids, hist, P, E, chunk);
   }
-  // small batches: no more waves than there are 64s of pairs
-  const int waves = std::max(1, std::min(kSortWaves, (std::min(P, chunk) + 63) / 64));
+  // small batches: no more waves than there are 64s of pairs, but four for the
+  // passes over the experts
+  const int waves = std::max(4, std::min(kSortWaves, (std::min(P, chunk) + 63) / 64));
   int id_bits = 0;
   while ((1 << id_bits) < E) ++id_bits;
   static const hipError_t attr =
       hipFuncSetAttribute(reinterpret_cast<const void*>(&k_moe_sort), hipFuncAttributeMaxDynamicSharedMemorySize,
-                          (kSortWaves + 1) * kMaxExperts * static_cast<int>(sizeof(int)));
+                          (kSortWaves + 2) * kMaxExperts * static_cast<int>(sizeof(int)));
   if (attr != hipSuccess) return BS_ERR_LAUNCH;
-  k_moe_sort<<<nb, 64 * waves, static_cast<size_t>(waves + 1) * E * sizeof(int), st>>>(ids, hist, rows, pos, offsets,
+  k_moe_sort<<<nb, 64 * waves, static_cast<size_t>(waves + 2) * E * sizeof(int), st>>>(ids, hist, rows, pos, offsets,
                                                                                       P, k, E, chunk, id_bits);
   return bs_launch_status();
 }

@@ -404,7 +404,7 @@ BS_API int dequant_mxfp4(const void* q, const void* scale, void* out, int M, int
  *   rows[s]     int32 [T * k] token of slot s, -1 for s >= offsets[E]
  * An expert may be chosen more than once by a token.  T >= 0 (with T == 0 only
  * offsets is written, with zeros), 1 <= E <= 1024, T * k <= 2^24.  More than
- * 8192 pairs need ws of bs_workspace_bytes(BS_OP_MOE_SORT, T, k, E) bytes
+ * 4096 pairs need ws of bs_workspace_bytes(BS_OP_MOE_SORT, T, k, E) bytes
  * (256-byte aligned; shared and zeroed like the other workspaces). */
 BS_API int moe_sort(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* offsets, int T, int k, int E, void* ws,
                     size_t ws_bytes, bs_stream_t stream);

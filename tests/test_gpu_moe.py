@@ -42,7 +42,8 @@ def _sort(ids, E):
 SORTS = [(1, 1, 1, 0, False), (1, 8, 256, 0, False), (8, 8, 256, 0, False), (3, 5, 7, .5, False), (64, 1, 2, 0, True),
          (65, 1, 1024, .2, False), (1000, 8, 256, .1, True), (1024, 8, 1000, 0, False), (1025, 8, 33, .3, False),
          (8191, 3, 256, 0, True), (40000, 8, 256, .25, False), (130001, 9, 64, 0, False), (7, 4, 16, 1.0, False),
-         (9000, 2, 5, 1.0, False)]
+         (9000, 2, 5, 1.0, False),
+         (4096, 1, 200, 0, False), (4097, 1, 200, .1, False), (2049, 2, 3, 0, True), (270000, 1, 40, .1, True)]
 
 
 @pytest.mark.parametrize("T,k,E,drop,skew", SORTS)

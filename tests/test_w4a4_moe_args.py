@@ -100,7 +100,7 @@ def test_moe_refusals(blib):
     assert s(FAKE, FAKE, FAKE, FAKE, 1 << 22, 5, 8, None, 0, None) == -2
     assert s(ODD, FAKE, FAKE, FAKE, 4, 2, 8, None, 0, None) == -3
     need = bs.workspace_bytes(bs.BS_OP_MOE_SORT, 5000, 2, 8)
-    assert need > 64 * 1024 and bs.workspace_bytes(bs.BS_OP_MOE_SORT, 4096, 2, 8) == 0
+    assert need > 64 * 1024 and bs.workspace_bytes(bs.BS_OP_MOE_SORT, 2048, 2, 8) == 0
     assert s(FAKE, FAKE, FAKE, FAKE, 5000, 2, 8, None, 0, None) == -5
     assert s(FAKE, FAKE, FAKE, FAKE, 5000, 2, 8, FAKE, need - 1, None) == -5
     assert s(FAKE, FAKE, FAKE, FAKE, 5000, 2, 8, ctypes.c_void_p(0x10040), need, None) == -3
