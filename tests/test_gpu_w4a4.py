@@ -25,10 +25,23 @@ def _dense(M, N, K, seed=0):
     return a, ae, w, we, pre, desc
 
 
-DENSE = [(1, 16, 128), (1, 5120, 640), (5, 272, 384), (8, 10240, 512), (16, 48, 5120), (16, 96, 12544), (17, 160, 1152),
-         (32, 256, 2048), (33, 144, 256), (64, 1040, 1280), (65, 16, 128), (65, 128, 1024), (100, 272, 2176),
-         (128, 128, 128), (129, 400, 384), (300, 1296, 640), (513, 144, 8192), (200, 2064, 512),
-         (1000, 528, 256)]
+# every configuration of the weight stream and every tile shape, K with and
+# without whole windows of 512 (the scale loads differ), ragged M and N
+DENSE = [
+    # weight stream, up to 16 rows: K = 512, 1024, 2048, 5120 (one run), longer (split)
+    (1, 16, 128), (8, 10240, 512), (3, 48, 1024), (7, 272, 768), (5, 272, 1664), (16, 48, 2048), (1, 5120, 2304),
+    (16, 48, 5120), (16, 96, 12544), (2, 16, 5248), (9, 4112, 2304), (12, 8208, 2304), (3, 4112, 12416),
+    # weight stream, 17 to 64 rows of long K
+    (20, 48, 12416), (33, 48, 12288), (64, 80, 12544),
+    # 64 x 64 tiles, two and four K groups
+    (17, 160, 1152), (32, 256, 2048), (33, 144, 256), (64, 1040, 1280), (65, 16, 128), (65, 128, 1024),
+    (100, 272, 2176), (128, 128, 128), (129, 400, 384), (300, 1296, 640), (513, 144, 8192), (200, 2064, 512),
+    (1000, 528, 256), (65, 144, 12416), (65, 144, 12288), (70, 64, 16384),
+    # 64 x 128 tiles
+    (513, 2064, 1024), (513, 2064, 896),
+    # 128 x 128 tiles
+    (1100, 2064, 1024),
+]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -46,7 +59,11 @@ def test_dense(M, N, K):
         assert torch.equal(c, c2)
 
 
-@pytest.mark.parametrize("M,N,K", [(4096, 4096, 1024), (3333, 5136, 640), (2048, 10240, 256), (700, 17408, 512)])
+@pytest.mark.parametrize("M,N,K", [
+    (4096, 4096, 1024), (3000, 5136, 512),       # 256 x 256 tiles
+    (3333, 5136, 640), (2048, 10240, 256),       # 128 x 128
+    (4352, 4240, 2048), (4352, 4240, 2176),      # 256 x 256 over whole rounds, the last columns 128 x 128
+])
 def test_dense_large_sampled(M, N, K):
     a, ae, w, we, pre, desc = _dense(M, N, K)
     c = bs.bsgemm_w4a4_mxfp4(dev_u8(a), dev_u8(ae), desc, pre, ws=bs.alloc_workspace(bs.BS_OP_W4A4_MXFP4, M, N, K))
@@ -58,13 +75,14 @@ def test_dense_large_sampled(M, N, K):
     mxfp4.assert_w4a4_close(got[rows], ce, asum, K, f"M={M} N={N} K={K}")
 
 
+@pytest.mark.parametrize("K", [640, 512])
 @pytest.mark.parametrize("M", [3, 40, 130])
-def test_dense_strides_and_guard(M):
+def test_dense_strides_and_guard(M, K):
     """Padded activation, scale and output rows; the padding keeps what it held."""
-    N, K = 272, 640
+    N = 272
     a, ae, w, we, pre, desc = _dense(M, N, K, 1)
     abuf = torch.full((M, K // 2 + 48), 0x77, dtype=torch.uint8, device="cuda")
-    sbuf = torch.full((M, K // 32 + 8), 0xFF, dtype=torch.uint8, device="cuda")   # NaN scales beside the used ones
+    sbuf = torch.full((M, K // 32 + 4), 0xFF, dtype=torch.uint8, device="cuda")   # NaN scales beside the used ones
     abuf[:, : K // 2] = dev_u8(a)
     sbuf[:, : K // 32] = dev_u8(ae)
     for ldc in (N + 4, N + 8):
