@@ -357,11 +357,11 @@ struct TileCfg {
   static constexpr int kSBIters = (kSBPieces + kWaves - 1) / kWaves, kSAIters = (kSAPieces + kWaves - 1) / kWaves;
   static constexpr int kDma = kAIters + kBIters, kWinDma = kSBIters + kSAIters;
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
-  static constexpr int kPassN = BN < 128 ? BN : 128;   // columns staged at once by the epilogue
   static constexpr int kGroup = kWin0 + kWLead * kWin;   // LDS of a group
   static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
-  static constexpr int kEpi = BM * kPassN * 4;
+  static constexpr int kEpi = WM * 32 * BN * 4;          // an epilogue pass: 32 rows of every wave
   static constexpr int kLds = std::max(KG * kGroup, std::max(kRed, kEpi));
+  static constexpr int kEpiBufs = 2 * kEpi <= kLds ? 2 : 1;
 };
 
 template <int V>
@@ -661,50 +661,53 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
     }
   }
 
-  // Epilogue: fp32 through LDS, kPassN columns of the tile at a time, so that
-  // each store instruction writes whole pieces of rows.  16-byte chunk q of a
-  // row sits at slot q ^ (row % 16).
-  constexpr int kPassN = C::kPassN, kPasses = BN / kPassN;
-  constexpr int kPP = C::kTN / kPasses;             // a wave's sub-tiles per pass
-  constexpr int kW = kPP * 32;                      // a wave's columns per pass
-  static_assert(WN * kW == kPassN && C::kTN % kPasses == 0, "");
-  constexpr int kLanes = kPassN / 8;                // lanes per row, 8 columns each
-  constexpr int kRows = C::kThreads * KG / kLanes;
-  static_assert(BM % kRows == 0, "");
+  // Epilogue: fp32 through LDS, 32 rows of every wave at a time (WM * 32 rows,
+  // all BN columns), so that a row leaves as whole 16-byte pieces side by side.
+  // 16-byte chunk q of a staged row sits at slot (q / 2 + (q odd ? BN / 8 : 0))
+  // ^ (row % 16): the 16 rows of a write phase and the 16 chunk pairs of a read
+  // phase each cover 16 distinct slots.  Where two passes fit, they alternate
+  // buffers and one pass's stores run under the next one's writes.
+  constexpr int kLanes = BN / 8, kRows = C::kThreads * KG / kLanes, kStaged = WM * 32;
   const int lane8 = tid % kLanes, rsub = tid / kLanes;
+  const bool n_ok = n0 + 8 * lane8 < N;   // N % 16 == 0: eight columns are wholly inside or outside
 #pragma unroll
-  for (int h = 0; h < kPasses; ++h) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (kg == 0)   // (the other groups have handed their sums over)
+  for (int j = 0; j < C::kTM; ++j) {
+    uint8_t* buf = lds + (C::kEpiBufs == 2 ? j & 1 : 0) * C::kEpi;
+    if (j == 0 || C::kEpiBufs == 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __syncthreads();   // the stages, or the pass before, are done with
+    }
+    if (kg == 0) {       // (the other groups have handed their sums over)
+      const int sr = wm * 32 + (l & 31);
+      uint8_t* rowp = buf + sr * (BN * 4);
 #pragma unroll
-    for (int j = 0; j < C::kTM; ++j) {
-      uint8_t* rowp = lds + arow[j] * (kPassN * 4);
-      const int x = arow[j] & 15;
-#pragma unroll
-      for (int i = 0; i < kPP; ++i)
+      for (int i = 0; i < C::kTN; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const v16f& av = acc[h * kPP + i][j];
-          const int q = wn * (kW / 4) + 8 * i + 2 * r + (l >> 5);
-          *reinterpret_cast<float4*>(rowp + ((q ^ x) << 4)) =
+          const v16f& av = acc[i][j];
+          const int q = (wn * (BN / WN) + 32 * i) / 4 + 2 * r + (l >> 5);   // odd exactly in the upper half wave
+          const int slot = ((q >> 1) + (l >> 5) * (BN / 8)) ^ (sr & 15);
+          *reinterpret_cast<float4*>(rowp + slot * 16) =
               make_float4(av[4 * r], av[4 * r + 1], av[4 * r + 2], av[4 * r + 3]);
         }
     }
     __syncthreads();
-    // staged column x of pass h is tile column (x / kW) * (BN / WN) + h * kW + x % kW
-    const int x0 = 4 * lane8, x1 = kPassN / 2 + 4 * lane8;
-    const int c0 = n0 + x0 / kW * (BN / WN) + h * kW + x0 % kW, c1 = n0 + x1 / kW * (BN / WN) + h * kW + x1 % kW;
 #pragma unroll 4
-    for (int r = rsub; r < BM; r += kRows) {
-      const uint8_t* rp = lds + r * (kPassN * 4);
-      const float4 u = *reinterpret_cast<const float4*>(rp + ((lane8 ^ (r & 15)) << 4));
-      const float4 v = *reinterpret_cast<const float4*>(rp + (((lane8 + kPassN / 8) ^ (r & 15)) << 4));
-      if (r < nrows) {
-        uint16_t* dst = p.c + (m0 + r) * p.ldc;
-        // N % 16 == 0: a piece of four columns is wholly inside or outside
-        if (c0 < N) st_stream8(reinterpret_cast<uint2*>(dst + c0), bf16x2_rne(u.x, u.y), bf16x2_rne(u.z, u.w));
-        if (c1 < N) st_stream8(reinterpret_cast<uint2*>(dst + c1), bf16x2_rne(v.x, v.y), bf16x2_rne(v.z, v.w));
+    for (int sr = rsub; sr < kStaged; sr += kRows) {
+      const uint8_t* rp = buf + sr * (BN * 4);
+      const float4 u = *reinterpret_cast<const float4*>(rp + ((lane8 ^ (sr & 15)) << 4));
+      const float4 v = *reinterpret_cast<const float4*>(rp + (((lane8 + BN / 8) ^ (sr & 15)) << 4));
+      const int r = (sr >> 5) * (BM / WM) + 32 * j + (sr & 31);
+      if (r < nrows && n_ok) {
+        uint16_t* dst = p.c + (m0 + r) * p.ldc + n0 + 8 * lane8;
+        const uint4 o =
+            make_uint4(bf16x2_rne(u.x, u.y), bf16x2_rne(u.z, u.w), bf16x2_rne(v.x, v.y), bf16x2_rne(v.z, v.w));
+        if (p.ldc % 8 == 0) {
+          st_stream16(reinterpret_cast<uint4*>(dst), o);
+        } else {
+          st_stream8(reinterpret_cast<uint2*>(dst), o.x, o.y);
+          st_stream8(reinterpret_cast<uint2*>(dst + 4), o.z, o.w);
+        }
       }
     }
   }
