@@ -8,13 +8,16 @@
 // mixed fp8 x fp4 form (about 9.7 PFLOP/s with registers only).  The weight
 // is the pre-laid-out MXFP4 weight of the W4A8 GEMM.
 //
-// Two kernels.  Few rows: a weight stream (k_w4a4_stream), bound by HBM.
-// Many rows: LDS-tiled (k_w4a4_tile), bound by the matrix cores, fed through
-// direct-to-LDS loads.  Both have a grouped form: the slots of the sorted
-// (token, expert) pairs are cut into row tiles expert by expert, and every
-// workgroup finds its tile from the expert offsets on the device, so the host
-// never waits for them; the activation rows are read through the sorted order
-// (row gather in the loads), never copied.
+// Two kernels.  Few rows: a weight stream (k_w4a4_stream), bound by HBM (M = 8
+// N = 17408 K = 5120: 10.4 us, 4.6 TB/s, where a large copy runs at 5.2).  Many
+// rows: LDS-tiled (k_w4a4_tile), fed through direct-to-LDS loads and bound by
+// the matrix cores' power: M = 8192 N = 10240 K = 5120 takes 199 us (4.3
+// PFLOP/s), 154 us when every code is zero, and 178 us with all loads and LDS
+// reads taken out of the loop.  Both have a grouped form: the slots of the
+// sorted (token, expert) pairs are cut into row tiles expert by expert, and
+// every workgroup finds its tile from the expert offsets on the device, so the
+// host never waits for them; the activation rows are read through the sorted
+// order (row gather in the loads), never copied.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -116,8 +119,8 @@ BS_INLINE int src_row(const W4A4Args& p, int slot) {
 BS_INLINE int swz4(int row, int chunk) { return chunk ^ ((row >> 2) & 3); }
 
 // grid (column groups, row tiles, K splits): workgroup (x, y, z) computes
-// n-tiles [x*TW*T, (x+1)*TW*T) of 16 columns for the 16*MB rows of row tile y
-// over its run of `iters * KW * R` K steps.  Wave (tw, kw) owns T tiles over R
+// n-tiles [x*TW*T, (x+1)*TW*T) of 16 columns for the up to 16*MB rows of row
+// tile y (dense: all rows) over its run of `iters * KW * R` K steps.  Wave (tw, kw) owns T tiles over R
 // steps of each KW*R; the KW partial sums of a tile are added through LDS in
 // kw order, K splits through the workspace.  The activation slice (KW*R steps
 // x rs rows x 64 B of codes and one scale dword per row and step) is copied to
@@ -146,8 +149,8 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
     w += static_cast<size_t>(e) * p.w_stride;
     wscb += static_cast<size_t>(e) * p.w_stride;
   } else {
-    m0 = blockIdx.y * 16 * MB;
-    nrows = min(RS, p.M - m0);
+    m0 = 0;
+    nrows = RS;
   }
   const uint32_t* wsc = reinterpret_cast<const uint32_t*>(wscb);
 
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
     const int ks0 = wg_k0 + kw * R;
     const int klast = min(ks0 + R, KS) - 1;  // below ks0 for an idle wave
     const int nsteps = klast - ks0 + 1;      // <= 0 for an idle wave
-    if (GROUPED && it) __syncthreads();                 // every wave is done with the slice
+    if (GROUPED && it) __syncthreads();      // every wave is done with the slice
     // chunk c of row i of step r sits at position (r*RS + i)*4 + swz4(i, c),
     // its scale dword at position r*RS + i; positions past the slice re-read
     // valid bytes that are never used
@@ -322,17 +325,20 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 // (BM x 64 B, chunks swizzled by swz4) and weight codes (BN/16 fragment blocks
 // of 1 KiB, as they are) go global -> LDS by direct loads into one of STAGES
 // buffers, STAGES - 1 steps ahead; the scales of a window (16 B per activation
-// row, 256 B per 16 columns) into a window buffer, WLEAD windows ahead.  The
-// steps of a window are unrolled, so the stage, the scale dword and its byte
-// are constants of the code, and a window's scales are read from LDS once,
-// under the last MFMAs of the window before.
+// row, 256 B per 16 columns) into a window buffer during the window before.
+// The steps of a window are unrolled, so the stage, the scale dword and its
+// byte are constants of the code, and a window's scales are read from LDS once,
+// under the last MFMAs of the window before.  (Reading and shifting a scale
+// dword at every half step stalled on each: M = 8192 N = 10240 K = 5120 237 us
+// instead of 201.)
 //
 // KG > 1: that many groups of WM x WN waves share the tile, each over every
 // KG-th window with buffers of its own, and their partial sums are added
 // through LDS in group order.  A step is a chain (barrier, LDS reads, MFMAs)
 // that one small wave tile per SIMD cannot hide; a second or fourth chain on
 // the same SIMD does, where splitting K over workgroups would send every
-// partial tile through memory.
+// partial tile through memory (M = 65 N = K = 5120: 64 x 128 tiles with two
+// groups 9.3 us, 128 x 128 tiles with K split over workgroups 12.9).
 //
 // AS16: the activation scale rows are 16-byte aligned and K is a multiple of
 // 512, so a row's window is one 16-byte load (rows of 16 B); otherwise it is
@@ -340,16 +346,12 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 // touched as many cache lines per step as the codes themselves.
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool AS16>
 struct TileCfg {
-  static constexpr int kStages = STAGES;
+  static_assert(STAGES == 3 || STAGES == 4, "the waits below");
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;   // of a group
   static constexpr int kTM = BM / WM / 32, kTN = BN / WN / 32;
   static constexpr int kA = BM * 64, kB = BN * 64, kStage = kA + kB;
   static constexpr int kSB = BN * 16, kSA = BM * 16, kWin = kSB + kSA;
-  static constexpr int kWin0 = kStages * kStage;       // the window buffers follow the stages
-  // a window's scales are read a window after they were loaded, or with more
-  // than four stages two windows after: always older by then than the loads
-  // that a step waits for
-  static constexpr int kWLead = STAGES > 4 ? 2 : 1;
+  static constexpr int kWin0 = STAGES * kStage;        // the window buffer follows the stages
   static constexpr int kAIters = kA / (kThreads * 16), kBIters = kB / (kThreads * 16);
   static constexpr int kSBPieces = kSB / 1024, kSAPieces = AS16 ? kSA / 1024 : kSA / 256;
   // loads per stage and per window, the same for every wave: a wave past a
@@ -357,7 +359,7 @@ struct TileCfg {
   static constexpr int kSBIters = (kSBPieces + kWaves - 1) / kWaves, kSAIters = (kSAPieces + kWaves - 1) / kWaves;
   static constexpr int kDma = kAIters + kBIters, kWinDma = kSBIters + kSAIters;
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
-  static constexpr int kGroup = kWin0 + kWLead * kWin;   // LDS of a group
+  static constexpr int kGroup = kWin0 + kWin;            // LDS of a group
   static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
   static constexpr int kEpi = WM * 32 * BN * 4;          // an epilogue pass: 32 rows of every wave
   static constexpr int kLds = std::max(KG * kGroup, std::max(kRed, kEpi));
@@ -438,10 +440,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
       dma16(base + C::kA + ((i - C::kAIters) * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024,
             boff_g[i - C::kAIters]);
   };
-  // the i-th load of the group's wi-th window into its buffer
+  // the i-th load of the scales of the group's wi-th window
   auto win_one = [&](int i, int wi) {
     const int win = win_of(wi);
-    const uint32_t base = lds0 + C::kWin0 + (C::kWLead == 2 ? (min(wi, n_win - 1) & 1) * C::kWin : 0);
+    const uint32_t base = lds0 + C::kWin0;
     if (i < C::kSBIters) {
       dma16(base + ((i * C::kWaves + wave) % C::kSBPieces) * 1024, wsc + static_cast<size_t>(win) * 256, sboff[i]);
     } else {
@@ -489,8 +491,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
       f.a[i - 1] = *reinterpret_cast<const v4i*>(base + abase[hh] + (i - 1) * 2048);
     }
   };
-  auto read_scale = [&](int wi, Scale& s, int i) {
-    const uint8_t* base = glds + C::kWin0 + (C::kWLead == 2 ? (min(wi, n_win - 1) & 1) * C::kWin : 0);
+  auto read_scale = [&](Scale& s, int i) {
+    const uint8_t* base = glds + C::kWin0;
     if (i < C::kTN) {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) s.b[i][hh] = *reinterpret_cast<const int*>(base + sbbase + i * 512 + hh * 128);
@@ -511,10 +513,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
   // lcm(4, STAGES), J = U % 4 its step of the window, U % STAGES its stage.
   // MFMAs of half HH of a step.  Between them: the LDS reads of the next half
   // (rf), this half's share of the loads of step dks (STAGES - 1 steps ahead),
-  // and in the step's second half the scale loads of window load_win (J = 0) or
-  // the reads of the next window's scales (J = 3).
-  auto half = [&](auto uu, auto hh, const Frag& f, Frag& rf, const Scale& s, int dks, int load_win, int next_win,
-                  Scale& ns) {
+  // and in the step's second half the loads of window next_win's scales (J = 0;
+  // the buffer's last reads were a step before) or their reads (J = 3).
+  auto half = [&](auto uu, auto hh, const Frag& f, Frag& rf, const Scale& s, int dks, int next_win, Scale& ns) {
     constexpr int U = decltype(uu)::value, HH = decltype(hh)::value, J = U % 4;
     constexpr int kRead = HH == 0 ? U % STAGES : (U + 1) % STAGES;
     constexpr int kN = C::kTN * C::kTM;
@@ -536,11 +537,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
         if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, (U + STAGES - 1) % STAGES);
       if (J == 0 && HH == 1 && n == kN - 1)
 #pragma unroll
-        for (int d = 0; d < C::kWinDma; ++d) win_one(d, load_win);
+        for (int d = 0; d < C::kWinDma; ++d) win_one(d, next_win);
       if (J == 3 && HH == 1) {
 #pragma unroll
         for (int d = 0; d < kPieces; ++d)
-          if (d * kN / kPieces == n) read_scale(next_win, ns, d);
+          if (d * kN / kPieces == n) read_scale(ns, d);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -561,29 +562,23 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
     for (int s = 0; s < STAGES - 1; ++s) {
 #pragma unroll
       for (int i = 0; i < C::kDma; ++i) dma_one(i, step_of(s), s);
-      // (with two windows of lead, the second is issued where step -4 would have)
-      if (C::kWLead == 2 && s == STAGES - 5)
-#pragma unroll
-        for (int d = 0; d < C::kWinDma; ++d) win_one(d, 1);
     }
   }
-  // newer than the first window and step 0: the other steps, and the second window
-  wait_vm<(STAGES - 2) * C::kDma + (C::kWLead == 2 ? C::kWinDma : 0)>();
+  wait_vm<(STAGES - 2) * C::kDma>();   // the first window and step 0 have landed
   __syncthreads();
   if (KG == 1 || n_win > 0) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) piece(0, 0, f0, i);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) read_scale(0, ns, i);
+    for (int i = 0; i < kPieces; ++i) read_scale(ns, i);
   }
   // step J of the group's wi-th window (live: it exists)
   auto step = [&](auto uu, int wi, bool live) {
     constexpr int U = decltype(uu)::value, J = U % 4;
     if (KG == 1 || live) {
-      // loads newer than step s+1's: STAGES - 3 steps, and the scale loads that
-      // the second halves of steps s-d (J = 0) issued, where they are newer
-      constexpr int kScaleEvents = (J >= 1 && J <= STAGES - 2 ? 1 : 0) + (J + 4 <= STAGES - 2 ? 1 : 0);
-      wait_vm<(STAGES - 3) * C::kDma + kScaleEvents * C::kWinDma>();
+      // loads newer than step s+1's: STAGES - 3 steps, and the window's scale
+      // loads (issued behind those of step STAGES - 1) in steps 1 .. STAGES - 2
+      wait_vm<(STAGES - 3) * C::kDma + (J >= 1 && J <= STAGES - 2 ? C::kWinDma : 0)>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     __syncthreads();
@@ -600,8 +595,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
         for (int hh = 0; hh < 2; ++hh) sc.b[t][hh] = ns.b[t][hh];
     }
     const int dks = step_of(4 * wi + J + STAGES - 1);
-    half(uu, Int<0>{}, f0, f1, sc, dks, wi + C::kWLead, wi + 1, ns);
-    half(uu, Int<1>{}, f1, f0, sc, dks, wi + C::kWLead, wi + 1, ns);
+    half(uu, Int<0>{}, f0, f1, sc, dks, wi + 1, ns);
+    half(uu, Int<1>{}, f1, f0, sc, dks, wi + 1, ns);
   };
   // (with one group, steps past the end are skipped; several groups meet at
   // every barrier, so those run it empty)
@@ -615,12 +610,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
     if (KG > 1 || k0 + 2 < KS) step(Int<W + 2>{}, wi, here && k0 + 2 < KS);
     if (KG > 1 || k0 + 3 < KS) step(Int<W + 3>{}, wi, here && k0 + 3 < KS);
   };
-  constexpr int kTurn = STAGES % 4 == 0 ? STAGES / 4 : (STAGES % 2 == 0 ? STAGES / 2 : STAGES);  // windows
-  static_assert(STAGES >= 3 && kTurn <= 3, "windows unrolled below");
+  constexpr int kTurn = STAGES == 4 ? 1 : 3;   // windows until the stages come round
   for (int wi = 0; wi < n_turns; wi += kTurn) {
     window(Int<0>{}, wi);
-    if constexpr (kTurn > 1) window(Int<1>{}, wi + 1);
-    if constexpr (kTurn > 2) window(Int<2>{}, wi + 2);
+    if constexpr (kTurn == 3) {
+      window(Int<1>{}, wi + 1);
+      window(Int<2>{}, wi + 2);
+    }
   }
   wait_vm<0>();
 
@@ -741,8 +737,8 @@ size_t stream_lds(const StreamCfg& d) {
 StreamCfg dense_stream_cfg(int M, int N, int KS) {
   StreamCfg d{};
   d.mb = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-  d.rs = std::min(M, 16 * d.mb);
-  d.mtiles = (M + 16 * d.mb - 1) / (16 * d.mb);
+  d.rs = M;
+  d.mtiles = 1;
   const int nt = N / 16;
   auto set = [&](int tw, int kw, int t, int r) { d.tw = tw; d.kw = kw; d.t = t; d.r = r; };
   if (d.mb > 1) set(8, 1, 1, 8);

@@ -183,7 +183,9 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict
 // A thread owns 8 columns (16 bytes) of a token: chunk c of nch.
 constexpr int kRT = 256;
 
-// xs[pos[t, j]] = x[t]: the token's row is read once and written k times.
+// xs[pos[t, j]] = x[t]: the token's row is read once and written k times (8192
+// tokens x 8 rows of 2048 52 us, 302 MB at 5.8 TB/s; without the streaming hint
+// on the stores 60).
 __global__ __launch_bounds__(kRT) void k_moe_gather(const uint4* __restrict__ x, const int* __restrict__ pos,
                                                     uint4* __restrict__ xs, uint32_t total, uint32_t nch, int k, int P) {
   const uint32_t i = blockIdx.x * kRT + threadIdx.x;
@@ -197,7 +199,11 @@ __global__ __launch_bounds__(kRT) void k_moe_gather(const uint4* __restrict__ x,
   }
 }
 
-constexpr int kJ = 8;   // expert rows whose loads are in flight together
+// Expert rows whose loads are in flight together.  The gradient holds two
+// addresses a row as well, in scalar registers: eight rows spill them (8192
+// tokens x 8 rows of 2048: 107 us with four, 570 MB at 5.3 TB/s; 108 with eight;
+// 2 rows of 5120: 68 and 72).
+constexpr int kJ = 8, kJb = 4;
 
 BS_INLINE void unpack_row(uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -209,6 +215,7 @@ BS_INLINE void unpack_row(uint4 v, float (&f)[8]) {
 }
 
 // out[t] = sum_j w[t, j] * y[pos[t, j]], fp32, in the order of j; one rounding.
+// Bound by HBM: 8192 tokens x 8 rows of 2048 53 us, 302 MB at 5.7 TB/s.
 // A dropped pair's load goes to row 0 and is not added (its row may hold
 // anything, NaN too).
 template <bool WEIGHTED>
@@ -232,9 +239,11 @@ __global__ __launch_bounds__(kRT) void k_moe_combine(const uint4* __restrict__ y
       if (j0 + j >= k || s[j] >= P) s[j] = -1;
     }
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) v[j] = ld_stream16(y + static_cast<size_t>(max(s[j], 0)) * nch + c);
+    for (int j = 0; j < kJ; ++j)
+      if (j0 + j < k) v[j] = ld_stream16(y + static_cast<size_t>(max(s[j], 0)) * nch + c);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
+      if (j0 + j >= k) break;
       float f[8];
       unpack_row(v[j], f);
 #pragma unroll
@@ -246,39 +255,43 @@ __global__ __launch_bounds__(kRT) void k_moe_combine(const uint4* __restrict__ y
 }
 
 // dy[pos[t, j]] = w[t, j] * dout[t] and dw[t, j] = <dout[t], y[pos[t, j]]>.
-// W waves share a token's columns; a lane's part of the dot product runs over
-// its chunks in order, then the lanes and the waves are added in a fixed order.
+// W waves share a token's columns (W = 1: four tokens to a workgroup); a lane's
+// part of the dot product runs over its chunks in order, then the lanes and the
+// waves are added in a fixed order.
 template <int W>
-__global__ __launch_bounds__(64 * W) void k_moe_combine_bwd(const uint4* __restrict__ dout,
-                                                            const uint4* __restrict__ y,
-                                                            const int* __restrict__ pos, const float* __restrict__ w,
-                                                            uint4* __restrict__ dy, float* __restrict__ dw,
-                                                            int nch, int k, int P) {
-  __shared__ float part[W][kJ];
-  const int t = blockIdx.x;
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+__global__ __launch_bounds__(kRT) void k_moe_combine_bwd(const uint4* __restrict__ dout, const uint4* __restrict__ y,
+                                                         const int* __restrict__ pos, const float* __restrict__ w,
+                                                         uint4* __restrict__ dy, float* __restrict__ dw, int T,
+                                                         int nch, int k, int P) {
+  static_assert(W == 1 || W == kRT / 64, "");
+  __shared__ float part[W][kJb];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int t = W == 1 ? blockIdx.x * (kRT / 64) + wave : blockIdx.x;
+  if (t >= T) return;
   const size_t p0 = static_cast<size_t>(t) * k;
   const uint4* drow = dout + static_cast<size_t>(t) * nch;
-  for (int j0 = 0; j0 < k; j0 += kJ) {
-    int s[kJ];
-    float wj[kJ], dot[kJ];
+  for (int j0 = 0; j0 < k; j0 += kJb) {
+    int s[kJb];
+    float wj[kJb], dot[kJb];
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
+    for (int j = 0; j < kJb; ++j) {
       const size_t p = p0 + min(j0 + j, k - 1);
       s[j] = pos[p];
       wj[j] = w[p];
       dot[j] = 0.0f;
       if (j0 + j >= k || s[j] >= P) s[j] = -1;
     }
-    for (int c = threadIdx.x; c < nch; c += 64 * W) {
+    for (int c = W == 1 ? l : static_cast<int>(threadIdx.x); c < nch; c += 64 * W) {
       const uint4 dv = drow[c];
-      uint4 v[kJ];
+      uint4 v[kJb];
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) v[j] = ld_stream16(y + static_cast<size_t>(max(s[j], 0)) * nch + c);
+      for (int j = 0; j < kJb; ++j)
+        if (j0 + j < k) v[j] = ld_stream16(y + static_cast<size_t>(max(s[j], 0)) * nch + c);
       float d[8];
       unpack_row(dv, d);
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
+      for (int j = 0; j < kJb; ++j) {
+        if (j0 + j >= k) break;
         float f[8];
         unpack_row(v[j], f);
 #pragma unroll
@@ -290,7 +303,7 @@ __global__ __launch_bounds__(64 * W) void k_moe_combine_bwd(const uint4* __restr
       }
     }
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
+    for (int j = 0; j < kJb; ++j) {
 #pragma unroll
       for (int o = 32; o >= 1; o >>= 1) dot[j] += __shfl_xor(dot[j], o, 64);
     }
@@ -298,18 +311,18 @@ __global__ __launch_bounds__(64 * W) void k_moe_combine_bwd(const uint4* __restr
       if (j0) __syncthreads();   // part is read below
       if (l == 0)
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) part[wave][j] = dot[j];
+        for (int j = 0; j < kJb; ++j) part[wave][j] = dot[j];
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
+      for (int j = 0; j < kJb; ++j) {
         dot[j] = part[0][j];
 #pragma unroll
         for (int v = 1; v < W; ++v) dot[j] += part[v][j];
       }
     }
-    if (threadIdx.x == 0)
+    if (W == 1 ? l == 0 : threadIdx.x == 0)
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+      for (int j = 0; j < kJb; ++j)
         if (j0 + j < k) dw[p0 + j0 + j] = s[j] >= 0 ? dot[j] : 0.0f;
   }
 }
@@ -395,8 +408,12 @@ BS_API int moe_combine_backward(const void* dout, const void* y, const int32_t* 
                bs_aligned(weights, 4) && bs_aligned(dweights, 4),
            BS_ERR_ALIGN);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  k_moe_combine_bwd<4><<<T, 256, 0, st>>>(static_cast<const uint4*>(dout), static_cast<const uint4*>(y), pos, weights,
-                                          static_cast<uint4*>(dy), dweights, K / 8, k, T * k);
+  const uint4 *dp = static_cast<const uint4*>(dout), *yp = static_cast<const uint4*>(y);
+  uint4* dyp = static_cast<uint4*>(dy);
+  // up to 1024 columns a wave takes a token alone (9 rows of 1024: 64 us against
+  // 74; one row of 64: 7 against 40; 8 rows of 2048: 126 against 107)
+  if (K <= 1024) k_moe_combine_bwd<1><<<(T + 3) / 4, kRT, 0, st>>>(dp, yp, pos, weights, dyp, dweights, T, K / 8, k, T * k);
+  else k_moe_combine_bwd<4><<<T, kRT, 0, st>>>(dp, yp, pos, weights, dyp, dweights, T, K / 8, k, T * k);
   return bs_launch_status();
 }
 
