@@ -896,14 +896,32 @@ int bs_launch_w4a4(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds
   return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, st);
 }
 
+// The weight stream over tiles of 16 rows and 16 * TW * T columns, KW * R steps
+// of K at a time.
+template <int TW, int KW, int T, int R>
+int launch_grouped_stream(W4A4Args& p, int S, hipStream_t st) {
+  const StreamCfg d{1,  TW, KW, T, R, 16, (p.N / 16 + TW * T - 1) / (TW * T), tile_bound(S, p.E, 16),
+                    1,  (p.KS + KW * R - 1) / (KW * R)};
+  return launch_stream<1, TW, KW, T, R, true>(d, p, st);
+}
+
 // Row tiles by S / E, the rows an expert would have if they were spread evenly
-// (swept at 256, 64 and 16 experts, S / E from 1/32 to 4096):
-//   - short K and few rows: the weight stream, whose workgroup covers 256
-//     columns (256 experts N = 2048 K = 512: S / E = 2 22 us against 27 with the
-//     tiles below, 8 28 against 31);
+// (swept at 256, 128, 64, 16 and 8 experts, S / E from 1/32 to 4096, weights
+// pooled past the last-level cache):
+//   - few rows (S / E < 16, from K = 1152 on < 10: at 12 rows the stream takes
+//     53 to 55 us against 52.6, at 8 49.6 against 51.9): the weight stream.  A
+//     workgroup of eight waves takes 256 columns with no K split, so that all
+//     its waves are busy at any K (256 experts N = 2048 K = 512, 64 rows of 8:
+//     22.4 us, 128 columns in two K groups 32.6; N = 1024 K = 2048, 128 rows
+//     23.1 against 24.1); 128 columns in two K groups where the grid is then
+//     two workgroups a CU or less, or K > 2048 (32 rows 9.9 us against 11.9; 64
+//     experts N = 1024 K = 5120, 32 rows 17.9 against 25.1, 512 rows 32.5
+//     against 34.8); 64 columns in four K groups where even that leaves half
+//     the CUs idle (8 rows of K = 2048 5.8 us against 7.1; 8 experts, one row of
+//     N = K = 4096 7.6 against 10.8);
 //   - up to 48 rows: 64 x 128 tiles, three workgroups a CU, whose loads run
-//     ahead over all of K (256 experts N = 1024 K = 2048: S / E = 2 40 us, the
-//     stream 42 to 45; 32 33 us, the tiles below 40);
+//     ahead over all of K (256 experts N = 1024 K = 2048, 16 rows 54 us, the
+//     stream 60; 32 rows 33 us from the cache, the tiles below 40);
 //   - above: 128 x 256 tiles, two workgroups a CU, so one's stores run under the
 //     other's MFMAs (S / E = 256 111 us; 128 x 128 131, 256 x 256 150).
 int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const int* offsets,
@@ -927,9 +945,11 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
   p.E = E;
   p.Ma = Ma;
   const int avg = S / E;
-  if (p.KS <= 8 && avg < 16) {
-    StreamCfg d{1, 8, 1, 2, 4, 16, (N / 16 + 15) / 16, tile_bound(S, E, 16), 1, (p.KS + 3) / 4};
-    return launch_stream<1, 8, 1, 2, 4, true>(d, p, st);
+  if (avg < (p.KS <= 8 ? 16 : 10)) {
+    const int64_t wgs = static_cast<int64_t>(tile_bound(S, E, 16)) * ((N + 127) / 128);
+    if (wgs <= 128 && p.KS > 8) return launch_grouped_stream<2, 4, 2, 4>(p, S, st);
+    if (p.KS > 16 || (wgs <= 512 && p.KS > 4)) return launch_grouped_stream<4, 2, 2, 4>(p, S, st);
+    return launch_grouped_stream<8, 1, 2, 4>(p, S, st);
   }
   if (avg <= 48)
     return launch_tile<64, 128, 1, 4, 1, 4, 3, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 127) / 128),

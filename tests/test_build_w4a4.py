@@ -39,7 +39,7 @@ def test_stream_waits_only_for_the_activation_loads():
         if m.group(6) == "0":
             assert min(waits) == allowed, f"{name}: a wait covers the weight loads: {waits}"
         seen += 1
-    assert seen == 10, seen
+    assert seen == 12, seen
 
 
 def test_tile_loop_keeps_loads_in_flight():

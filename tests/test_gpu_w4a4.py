@@ -170,6 +170,21 @@ def test_grouped(counts, N, K, Ma):
     _grouped(counts, N, K, Ma, seed=2, with_rows=False)
 
 
+@pytest.mark.parametrize("E,N,K", [
+    (3, 80, 2304),     # few workgroups: four K groups, the second run of K steps partly idle
+    (4, 144, 896),     # two K groups that cover all of K
+    (70, 272, 2176),   # two K groups, runs of 8 steps, one in the last
+    (70, 1040, 1152),  # no K groups, runs of 4 steps
+    (70, 48, 384)])
+def test_grouped_few_rows(E, N, K):
+    """The weight stream's forms, at most 9 rows an expert on average, some with more."""
+    g = np.random.default_rng(E + N)
+    counts = np.where(g.random(E) < 0.8, g.integers(1, 5, E), 0)
+    counts[E // 2] = 18
+    _grouped(counts.tolist(), N, K, 11)
+    _grouped(counts.tolist(), N, K, 5, tail=3, seed=1)
+
+
 def test_grouped_many_experts():
     """More experts than one pass of the tile search covers, most of them empty."""
     g = np.random.default_rng(6)
