@@ -659,6 +659,8 @@ def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
     _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, fn, "ids must be a 2-D tensor [T, k]")
     T, k = ids.shape
     _arg(fn, "ids", ids, (T, k), _I32, unit_inner=False)
+    if not (isinstance(E, int) and E >= 1):
+        _need(False, fn, f"E = {E!r} must be a positive int")
     dev = ids.device
     if rows is None:
         rows = torch.empty((T * k,), dtype=torch.int32, device=dev)

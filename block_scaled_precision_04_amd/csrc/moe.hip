@@ -164,7 +164,8 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict
     if (keep) {
       const int rank = __popcll(same & ((1ull << l) - 1));
       const int slot = tot[id] + cnt[wave * E + id] + rank;
-      rows[slot] = p / k;
+      // (counts overwritten by another call that shares ws unordered name no slot outside)
+      if (static_cast<unsigned>(slot) < static_cast<unsigned>(P)) rows[slot] = p / k;
       pos[p] = slot;
       wave_lds_fence();   // every lane has read its count
       if ((same >> l) == 1) cnt[wave * E + id] += rank + 1;   // the expert's last lane

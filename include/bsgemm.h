@@ -268,9 +268,9 @@ BS_API int gemm_bf16_skinny_noalloc(const void* x, const void* w, void* c, int M
  * c: bf16 [M, N] (ldc elements, multiple of 4).  Needs 1 <= M <= 2^22,
  * N % 16 == 0, K % 128 == 0; a, c 16-byte, a_scale 4-byte, w_pre 256-byte
  * aligned; M * lda, M * ld_scale and N * K / 2 < 2^32.
- * Up to 64 rows a weight stream runs, above an LDS-tiled kernel; either may
- * split K through ws of bs_workspace_bytes(BS_OP_W4A4_MXFP4, M, N, K) bytes
- * (256-byte aligned, zeroed once); when that is 0, ws may be NULL. */
+ * Few rows (at most 64) run a weight stream, more an LDS-tiled kernel; the
+ * stream may split K through ws of bs_workspace_bytes(BS_OP_W4A4_MXFP4, M, N,
+ * K) bytes (256-byte aligned, zeroed once); when that is 0, ws may be NULL. */
 BS_API int bsgemm_w4a4_mxfp4(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, const bs_wdesc* wd,
                              const void* w_pre, void* c, int64_t ldc, int M, int N, int K, void* ws, size_t ws_bytes,
                              bs_stream_t stream);
@@ -392,8 +392,9 @@ BS_API int silu_mul_quant_mxfp4(const void* gu, void* q, void* scale, const int3
 BS_API int dequant_mxfp4(const void* q, const void* scale, void* out, int M, int K, bs_stream_t stream);
 
 /* ------------------------------------------------- mixture of experts
- * Pair p = t * k + j is the j-th choice of token t.  Every sum below runs in
- * the order of j and every result is deterministic. */
+ * Pair p = t * k + j is the j-th choice of token t.  Every sum over j runs in
+ * its order and every result is deterministic.  Outputs overlap neither inputs
+ * nor each other. */
 
 /* Sort the pairs by expert (stable: equal ids keep the order of p).
  * ids: int32 [T, k]; a pair whose id is outside [0, E) is dropped (a padded
@@ -426,8 +427,7 @@ BS_API int moe_combine(const void* y, const int32_t* pos, const float* weights, 
 /* The gradient of moe_combine for dout = d/d out (bf16 [T, K]):
  *   dy[pos[t, j], :] = bf16( weights[t, j] * dout[t, :] )   other rows of dy are left as they are
  *   dweights[t, j]   = sum_c dout[t, c] * y[pos[t, j], c]   fp32; 0 for a dropped pair
- * pos has to name every slot at most once, as moe_sort writes it.  No overlap
- * between inputs and outputs. */
+ * pos has to name every slot at most once, as moe_sort writes it. */
 BS_API int moe_combine_backward(const void* dout, const void* y, const int32_t* pos, const float* weights, void* dy,
                                 float* dweights, int T, int k, int K, bs_stream_t stream);
 

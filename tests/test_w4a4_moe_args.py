@@ -157,6 +157,8 @@ def test_binding_refusals():
     ids = torch.zeros((4, 2), dtype=i32)
     _refused(bs.moe_sort, "ids has dtype", ids.long(), 8)
     _refused(bs.moe_sort, "pos has shape", ids, 8, pos=torch.zeros((2, 4), dtype=i32))
+    _refused(bs.moe_sort, "positive int", ids, -1)
+    _refused(bs.moe_sort, "positive int", ids, 8.0)
     _refused(bs.moe_sort, "on a GPU", ids, 8)
     y = torch.zeros((8, 64), dtype=bf)
     _refused(bs.moe_gather, "x has shape", y, ids)
