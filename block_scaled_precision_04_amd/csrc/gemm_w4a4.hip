@@ -358,6 +358,7 @@ struct TileCfg {
   // section's last piece repeats an earlier one (same bytes, same place)
   static constexpr int kSBIters = (kSBPieces + kWaves - 1) / kWaves, kSAIters = (kSAPieces + kWaves - 1) / kWaves;
   static constexpr int kDma = kAIters + kBIters, kWinDma = kSBIters + kSAIters;
+  static constexpr int kDmaFirst = (kDma + 1) / 2;      // of them, in the half step that frees the stage
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
   static constexpr int kGroup = kWin0 + kWin;            // LDS of a group
   static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
@@ -511,15 +512,17 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
   };
   // Place of a step in the unrolled turn: U is the step's index modulo
   // lcm(4, STAGES), J = U % 4 its step of the window, U % STAGES its stage.
-  // MFMAs of half HH of a step.  Between them: the LDS reads of the next half
-  // (rf), this half's share of the loads of step dks (STAGES - 1 steps ahead),
-  // and in the step's second half the loads of window next_win's scales (J = 0;
-  // the buffer's last reads were a step before) or their reads (J = 3).
+  // MFMAs of half HH of a step s.  Between them: the LDS reads of the next half
+  // (rf), half of a step's loads (HH 0: the rest of step s + STAGES - 1's; HH 1:
+  // the first of step s + STAGES's, whose stage has just become free), and in the
+  // step's second half the loads of window next_win's scales (J = 0; the buffer's
+  // last reads were a step before) or their reads (J = 3).
   auto half = [&](auto uu, auto hh, const Frag& f, Frag& rf, const Scale& s, int dks, int next_win, Scale& ns) {
     constexpr int U = decltype(uu)::value, HH = decltype(hh)::value, J = U % 4;
     constexpr int kRead = HH == 0 ? U % STAGES : (U + 1) % STAGES;
     constexpr int kN = C::kTN * C::kTM;
-    constexpr int d0 = HH * ((C::kDma + 1) / 2), d1 = HH ? C::kDma : (C::kDma + 1) / 2;
+    constexpr int d0 = HH ? 0 : C::kDmaFirst, d1 = HH ? C::kDmaFirst : C::kDma;
+    constexpr int kFill = HH ? U % STAGES : (U + STAGES - 1) % STAGES;
 #pragma unroll
     for (int n = 0; n < kN || n < kPieces; ++n) {
       if (n < kN) {
@@ -534,7 +537,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
       // the loads, spread evenly over the half's MFMAs
 #pragma unroll
       for (int d = d0; d < d1; ++d)
-        if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, (U + STAGES - 1) % STAGES);
+        if ((d - d0) * kN / (d1 - d0) == n) dma_one(d, dks, kFill);
       if (J == 0 && HH == 1 && n == kN - 1)
 #pragma unroll
         for (int d = 0; d < C::kWinDma; ++d) win_one(d, next_win);
@@ -547,8 +550,12 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
     }
   };
 
-  // Step s: this wave's loads of step s+1 have landed and its LDS reads are
-  // done; barrier (s+1 published, the stage of s-1 free); then the two halves.
+  // Step s: first half; this wave's loads of step s+1 have landed and its LDS
+  // reads are done; barrier (s+1 published, the stage of s free); second half,
+  // which reads s+1's first fragments.  So a stage is filled again right behind
+  // its last reads and waited for only where it is read, STAGES - 1 steps later
+  // (with the barrier in front of both halves, half a step is lost at each end:
+  // 256 experts N = 1024 K = 2048, 65536 rows XXX us instead of 121).
   // Steps and windows past the end re-load the last one (never used, or the
   // same bytes).
   Frag f0, f1;
@@ -563,8 +570,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
 #pragma unroll
       for (int i = 0; i < C::kDma; ++i) dma_one(i, step_of(s), s);
     }
+#pragma unroll
+    for (int i = 0; i < C::kDmaFirst; ++i) dma_one(i, step_of(STAGES - 1), STAGES - 1);
   }
-  wait_vm<(STAGES - 2) * C::kDma>();   // the first window and step 0 have landed
+  wait_vm<(STAGES - 2) * C::kDma + C::kDmaFirst>();   // the first window and step 0 have landed
   __syncthreads();
   if (KG == 1 || n_win > 0) {
 #pragma unroll
@@ -576,27 +585,26 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
   auto step = [&](auto uu, int wi, bool live) {
     constexpr int U = decltype(uu)::value, J = U % 4;
     if (KG == 1 || live) {
-      // loads newer than step s+1's: STAGES - 3 steps, and the window's scale
-      // loads (issued behind those of step STAGES - 1) in steps 1 .. STAGES - 2
-      wait_vm<(STAGES - 3) * C::kDma + (J >= 1 && J <= STAGES - 2 ? C::kWinDma : 0)>();
+      if constexpr (J == 0) {
+#pragma unroll
+        for (int t = 0; t < C::kTM; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc.a[t][j] = static_cast<int>(static_cast<uint32_t>(ns.a[t][j]) >> sh_a);
+#pragma unroll
+        for (int t = 0; t < C::kTN; ++t)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) sc.b[t][hh] = ns.b[t][hh];
+      }
+      half(uu, Int<0>{}, f0, f1, sc, step_of(4 * wi + J + STAGES - 1), wi + 1, ns);
+      // loads newer than step s+1's: STAGES - 2 steps, and the window's scale
+      // loads (issued behind the first of step STAGES) in steps 1 .. STAGES - 2
+      wait_vm<(STAGES - 2) * C::kDma + (J >= 1 && J <= STAGES - 2 ? C::kWinDma : 0)>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     if (KG > 1 && !live) return;
-    if constexpr (J == 0) {
-#pragma unroll
-      for (int t = 0; t < C::kTM; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc.a[t][j] = static_cast<int>(static_cast<uint32_t>(ns.a[t][j]) >> sh_a);
-#pragma unroll
-      for (int t = 0; t < C::kTN; ++t)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) sc.b[t][hh] = ns.b[t][hh];
-    }
-    const int dks = step_of(4 * wi + J + STAGES - 1);
-    half(uu, Int<0>{}, f0, f1, sc, dks, wi + 1, ns);
-    half(uu, Int<1>{}, f1, f0, sc, dks, wi + 1, ns);
+    half(uu, Int<1>{}, f1, f0, sc, step_of(4 * wi + J + STAGES), wi + 1, ns);
   };
   // (with one group, steps past the end are skipped; several groups meet at
   // every barrier, so those run it empty)

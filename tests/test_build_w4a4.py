@@ -54,7 +54,7 @@ def test_tile_loop_keeps_loads_in_flight():
         first = next(i for i, s in enumerate(ins) if s.startswith("v_mfma"))
         last = max(i for i, s in enumerate(ins) if s.startswith("v_mfma"))
         waits = [w for w in map(_vmcnt, (s for s in ins[first:last] if s.startswith("s_waitcnt"))) if w is not None]
-        base = (stages - 3) * dma
+        base = (stages - 2) * dma
         assert waits and set(waits) <= {base, base + win}, f"{name}: waits {sorted(set(waits))}, want {base}, {base + win}"
         run = longest = 0
         for s in ins[first:last + 1]:
