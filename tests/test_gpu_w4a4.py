@@ -185,6 +185,14 @@ def test_grouped_few_rows(E, N, K):
     _grouped(counts.tolist(), N, K, 5, tail=3, seed=1)
 
 
+@pytest.mark.parametrize("N,K", [(80, 256), (528, 384), (2048, 128)])
+def test_grouped_many_row_tiles(N, K):
+    """Enough row tiles that runs of them go to one XCD, with a rest that does not."""
+    counts = [300, 129, 0, 512, 257, 1, 640, 128, 127, 400, 0, 383, 5, 700]
+    _grouped(counts, N, K, 222)
+    _grouped(counts, N, K, 222, tail=200, seed=1)
+
+
 def test_grouped_many_experts():
     """More experts than one pass of the tile search covers, most of them empty."""
     g = np.random.default_rng(6)
