@@ -335,10 +335,10 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 // KG > 1: that many groups of WM x WN waves share the tile, each over every
 // KG-th window with buffers of its own, and their partial sums are added
 // through LDS in group order.  A step is a chain (barrier, LDS reads, MFMAs)
-// that one small wave tile per SIMD cannot hide; a second or fourth chain on
-// the same SIMD does, where splitting K over workgroups would send every
-// partial tile through memory (M = 65 N = K = 5120: 64 x 128 tiles with two
-// groups 9.3 us, 128 x 128 tiles with K split over workgroups 12.9).
+// that one small wave tile per SIMD cannot hide; a second chain on the same
+// SIMD does, where splitting K over workgroups would send every partial tile
+// through memory (M = 65 N = K = 5120: 64 x 128 tiles with two groups 9.3 us,
+// 128 x 128 tiles with K split over workgroups 12.9).
 //
 // AS16: the activation scale rows are 16-byte aligned and K is a multiple of
 // 512, so a row's window is one 16-byte load (rows of 16 B); otherwise it is
@@ -735,11 +735,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
 // ---------------------------------------------------------------- host side
 constexpr size_t kMaxStreamLds = 160 * 1024 - 256;
 
-// The weight stream takes up to 16 rows, and up to 64 where K is long and N
-// narrow (K >= 12288, N < 8192): there its K splits over workgroups keep more
-// of the GPU loading than the tiles' K groups (M = 48 N = 5120 K = 17408 23.8
-// us against 29.3, but N = 10240 38.3 against 31.4, and N = K = 5120 11.0
-// against 8.5).
+// The weight stream takes up to 16 rows (M = 16 N = K = 5120 6.3 us, tiles 8.9),
+// and up to 64 where K is long and N narrow (K >= 12288, N < 8192): there its K
+// splits over workgroups keep more of the GPU loading than the tiles' K groups
+// (M = 48: N = 5120 K = 17408 24.4 us against 28.5; N = 7168 K = 12288 22.0
+// against 21.6).
 bool use_stream(int M, int N, int KS) { return M <= 16 || (M <= 64 && KS >= 96 && N < 8192); }
 
 struct StreamCfg {
@@ -828,25 +828,31 @@ int launch_tile(const W4A4Args& p, int64_t wgs, hipStream_t st) {
 // The dense tile shapes and what a launch of each takes, in us: with x = tiles
 // / 256 (one per CU) and R = ceil(x) rounds,
 //   t = start + R * (round + steps * step) + x * steps * load
-// least squares over 14 row counts from 32 to 4096, N = 512 .. 17408 and
-// K = 512 .. 17408 (rms 5 to 9%; the shape with the smallest t is the measured
-// best or within 1% of it, at worst 13%).
+// least squares over 13 row counts from 24 to 4096 at eight N x K, N = 1024 ..
+// 17408 and K = 1024 .. 17408, weights pooled past the last-level cache (rms 10
+// to 14%, less where a shape is near the best; the shape with the smallest t is
+// the measured best or within 1% of it in 100 of the 104, at worst 7%).  128 x
+// 256, whose two workgroups fill a CU's LDS, takes over between half a round
+// and one of the large tiles (M = 1024 N = K = 5120 29.1 us, 128 x 128 36.8, 256
+// x 256 41.0).  With exactly 256 workgroups of it some CUs get two and others
+// none (M = 2048 N = 4096 K = 1024 15.2 us; 192 of them 8.9): two rounds.
 struct TileShape {
   int bm, bn;
   float start, round, step, load;
 };
 constexpr TileShape kTiles[] = {
-    {256, 256, 0.0f, 7.93f, 0.453f, 0.356f},  // 4 waves of 128 x 128
-    {128, 128, 2.35f, 1.19f, 0.171f, 0.146f}, // 4 waves of 64 x 64, two workgroups a CU
-    {64, 128, 1.44f, 2.25f, 0.118f, 0.092f},  // 2 K groups of 4 waves of 64 x 32
-    {64, 64, 2.47f, 0.83f, 0.075f, 0.055f},   // 2 K groups of 2 waves of 64 x 32, two workgroups a CU
-    {64, 64, 1.62f, 2.32f, 0.066f, 0.079f},   // 4 K groups of the same
+    {256, 256, 0.90f, 6.98f, 0.512f, 0.517f}, // 4 waves of 128 x 128
+    {128, 256, 3.71f, 0.38f, 0.385f, 0.286f}, // 4 waves of 64 x 128, two workgroups a CU
+    {128, 128, 2.36f, 0.43f, 0.283f, 0.159f}, // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 1.58f, 1.67f, 0.188f, 0.116f},  // 2 K groups of 4 waves of 64 x 32
+    {64, 64, 2.42f, 0.30f, 0.134f, 0.060f},   // 2 K groups of 2 waves of 64 x 32, two workgroups a CU
 };
 float tile_cost(int i, int M, int N, int KS) {
   const TileShape& t = kTiles[i];
   const int64_t tiles = static_cast<int64_t>((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
   const float x = static_cast<float>(tiles) / 256.0f;
-  return t.start + std::ceil(x) * (t.round + KS * t.step) + x * KS * t.load;
+  const float rounds = i == 1 && tiles == 256 ? 2.0f : std::ceil(x);
+  return t.start + rounds * (t.round + KS * t.step) + x * KS * t.load;
 }
 int best_tile(int M, int N, int KS) {
   int best = 0;
@@ -867,10 +873,10 @@ int run_tiles(int i, const W4A4Args& q, int n0, int n1, hipStream_t st) {
       static_cast<int64_t>((p.M + kTiles[i].bm - 1) / kTiles[i].bm) * ((p.N + kTiles[i].bn - 1) / kTiles[i].bn);
   switch (i) {
     case 0: return launch_tile<256, 256, 2, 2, 1, 4, 1, false>(p, wgs, st);
-    case 1: return launch_tile<128, 128, 2, 2, 1, 4, 2, false>(p, wgs, st);
-    case 2: return launch_tile<64, 128, 1, 4, 2, 4, 2, false>(p, wgs, st);
-    case 3: return launch_tile<64, 64, 1, 2, 2, 4, 2, false>(p, wgs, st);
-    default: return launch_tile<64, 64, 1, 2, 4, 4, 2, false>(p, wgs, st);
+    case 1: return launch_tile<128, 256, 2, 2, 1, 3, 2, false>(p, wgs, st);
+    case 2: return launch_tile<128, 128, 2, 2, 1, 4, 2, false>(p, wgs, st);
+    case 3: return launch_tile<64, 128, 1, 4, 2, 4, 2, false>(p, wgs, st);
+    default: return launch_tile<64, 64, 1, 2, 2, 4, 2, false>(p, wgs, st);
   }
 }
 
@@ -946,7 +952,8 @@ int launch_grouped_stream(W4A4Args& p, int S, hipStream_t st) {
 //     ahead over all of K (256 experts N = 1024 K = 2048, 16 rows 54 us, the
 //     stream 60; 32 rows 33 us from the cache, the tiles below 40);
 //   - above: 128 x 256 tiles, two workgroups a CU, so one's stores run under the
-//     other's MFMAs (S / E = 256 111 us; 128 x 128 131, 256 x 256 150).
+//     other's MFMAs (256 experts N = 1024 K = 2048, 65536 rows 118 us; 128 x 128
+//     144, 256 x 256 142, which gains from 2000 rows of K = 7168 on only, 7%).
 int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const int* offsets,
                            const int* rows, const uint8_t* w, size_t w_scales, size_t w_stride, uint16_t* c,
                            int64_t ldc, int S, int Ma, int E, int N, int K, hipStream_t st) {

@@ -33,7 +33,7 @@ DENSE = [
     (16, 48, 5120), (16, 96, 12544), (2, 16, 5248), (9, 4112, 2304), (12, 8208, 2304), (3, 4112, 12416),
     # weight stream, 17 to 64 rows of long K
     (20, 48, 12416), (33, 48, 12288), (64, 80, 12544),
-    # 64 x 64 tiles, two and four K groups
+    # 64 x 64 tiles
     (17, 160, 1152), (32, 256, 2048), (33, 144, 256), (64, 1040, 1280), (65, 16, 128), (65, 128, 1024),
     (100, 272, 2176), (128, 128, 128), (129, 400, 384), (300, 1296, 640), (513, 144, 8192), (200, 2064, 512),
     (1000, 528, 256), (65, 144, 12416), (65, 144, 12288), (70, 64, 16384),
@@ -41,6 +41,8 @@ DENSE = [
     (513, 2064, 1024), (513, 2064, 896),
     # 128 x 128 tiles
     (1100, 2064, 1024),
+    # 128 x 256 tiles
+    (1000, 4112, 640), (900, 4112, 1024),
 ]
 
 
@@ -60,9 +62,9 @@ def test_dense(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [
-    (4096, 4096, 1024), (3000, 5136, 512),       # 256 x 256 tiles
-    (3333, 5136, 640), (2048, 10240, 256),       # 128 x 128
-    (4352, 4240, 2048), (4352, 4240, 2176),      # 256 x 256 over whole rounds, the last columns 128 x 128
+    (4096, 4096, 1024), (3000, 5136, 512), (3333, 5136, 640), (2048, 10240, 256), (4352, 4240, 2048),  # 128 x 256
+    (1025, 10256, 2048), (1025, 10256, 2176),    # 256 x 256
+    (4352, 4240, 2176), (2048, 9008, 2048),      # 256 x 256 over whole rounds, the last columns smaller tiles
 ])
 def test_dense_large_sampled(M, N, K):
     a, ae, w, we, pre, desc = _dense(M, N, K)
