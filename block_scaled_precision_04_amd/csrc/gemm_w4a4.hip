@@ -11,9 +11,9 @@
 // Two kernels.  Few rows: a weight stream (k_w4a4_stream), bound by HBM (M = 8
 // N = 17408 K = 5120: 10.4 us, 4.6 TB/s, where a large copy runs at 5.2).  Many
 // rows: LDS-tiled (k_w4a4_tile), fed through direct-to-LDS loads and bound by
-// the matrix cores' power: M = 8192 N = 10240 K = 5120 takes 199 us (4.3
-// PFLOP/s), 154 us when every code is zero, and 178 us with all loads and LDS
-// reads taken out of the loop.  Both have a grouped form: the slots of the
+// the matrix cores' power: M = 8192 N = 10240 K = 5120 takes 200 to 213 us by
+// card (4.0 to 4.3 PFLOP/s), 154 us when every code is zero, and 178 us with all
+// loads and LDS reads taken out of the loop.  Both have a grouped form: the slots of the
 // sorted (token, expert) pairs are cut into row tiles expert by expert, and
 // every workgroup finds its tile from the expert offsets on the device, so the
 // host never waits for them; the activation rows are read through the sorted
@@ -362,9 +362,8 @@ struct TileCfg {
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0 && kSB % 1024 == 0 && kSA % 1024 == 0, "");
   static constexpr int kGroup = kWin0 + kWin;            // LDS of a group
   static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
-  static constexpr int kEpi = WM * 32 * BN * 4;          // an epilogue pass: 32 rows of every wave
+  static constexpr int kEpi = BM * BN * 2;               // the epilogue's tile
   static constexpr int kLds = std::max(KG * kGroup, std::max(kRed, kEpi));
-  static constexpr int kEpiBufs = 2 * kEpi <= kLds ? 2 : 1;
 };
 
 // Workgroup -> grouped tile (row tile id / n_tiles, columns id % n_tiles).
@@ -680,54 +679,40 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
     }
   }
 
-  // Epilogue: fp32 through LDS, 32 rows of every wave at a time (WM * 32 rows,
-  // all BN columns), so that a row leaves as whole 16-byte pieces side by side.
-  // 16-byte chunk q of a staged row sits at slot (q / 2 + (q odd ? BN / 8 : 0))
-  // ^ (row % 16): the 16 rows of a write phase and the 16 chunk pairs of a read
-  // phase each cover 16 distinct slots.  Where two passes fit, they alternate
-  // buffers and one pass's stores run under the next one's writes.
-  constexpr int kLanes = BN / 8, kRows = C::kThreads * KG / kLanes, kStaged = WM * 32;
-  const int lane8 = tid % kLanes, rsub = tid / kLanes;
-  const bool n_ok = n0 + 8 * lane8 < N;   // N % 16 == 0: eight columns are wholly inside or outside
+  // Epilogue: the tile through LDS as bf16, so that a row leaves as whole
+  // 16-byte pieces side by side.  A lane's four columns are half a piece; piece
+  // q of a row sits at slot q ^ (row % pieces), which spreads a write's 32 rows
+  // over all banks.
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __syncthreads();       // the stages are done with
+  constexpr int kLanes = BN / 8, kRows = C::kThreads * KG / kLanes;   // pieces of a row, rows at once
+  if (kg == 0) {         // (the other groups have handed their sums over)
 #pragma unroll
-  for (int j = 0; j < C::kTM; ++j) {
-    uint8_t* buf = lds + (C::kEpiBufs == 2 ? j & 1 : 0) * C::kEpi;
-    if (j == 0 || C::kEpiBufs == 1) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __syncthreads();   // the stages, or the pass before, are done with
-    }
-    if (kg == 0) {       // (the other groups have handed their sums over)
-      const int sr = wm * 32 + (l & 31);
-      uint8_t* rowp = buf + sr * (BN * 4);
+    for (int j = 0; j < C::kTM; ++j) {
+      const int row = arow[j];
 #pragma unroll
       for (int i = 0; i < C::kTN; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const v16f& av = acc[i][j];
-          const int q = (wn * (BN / WN) + 32 * i) / 4 + 2 * r + (l >> 5);   // odd exactly in the upper half wave
-          const int slot = ((q >> 1) + (l >> 5) * (BN / 8)) ^ (sr & 15);
-          *reinterpret_cast<float4*>(rowp + slot * 16) =
-              make_float4(av[4 * r], av[4 * r + 1], av[4 * r + 2], av[4 * r + 3]);
+          const int q = (wn * (BN / WN) + 32 * i) / 8 + r;
+          *reinterpret_cast<uint2*>(lds + row * (BN * 2) + ((q ^ (row % kLanes)) << 4) + 8 * (l >> 5)) =
+              uint2{bf16x2_rne(av[4 * r], av[4 * r + 1]), bf16x2_rne(av[4 * r + 2], av[4 * r + 3])};
         }
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  const int q = tid % kLanes;
+  if (n0 + 8 * q >= N) return;   // N % 16 == 0: eight columns are wholly inside or outside
 #pragma unroll 4
-    for (int sr = rsub; sr < kStaged; sr += kRows) {
-      const uint8_t* rp = buf + sr * (BN * 4);
-      const float4 u = *reinterpret_cast<const float4*>(rp + ((lane8 ^ (sr & 15)) << 4));
-      const float4 v = *reinterpret_cast<const float4*>(rp + (((lane8 + BN / 8) ^ (sr & 15)) << 4));
-      const int r = (sr >> 5) * (BM / WM) + 32 * j + (sr & 31);
-      if (r < nrows && n_ok) {
-        uint16_t* dst = p.c + (m0 + r) * p.ldc + n0 + 8 * lane8;
-        const uint4 o =
-            make_uint4(bf16x2_rne(u.x, u.y), bf16x2_rne(u.z, u.w), bf16x2_rne(v.x, v.y), bf16x2_rne(v.z, v.w));
-        if (p.ldc % 8 == 0) {
-          st_stream16(reinterpret_cast<uint4*>(dst), o);
-        } else {
-          st_stream8(reinterpret_cast<uint2*>(dst), o.x, o.y);
-          st_stream8(reinterpret_cast<uint2*>(dst + 4), o.z, o.w);
-        }
-      }
+  for (int r = tid / kLanes; r < nrows; r += kRows) {
+    const uint4 o = *reinterpret_cast<const uint4*>(lds + r * (BN * 2) + ((q ^ (r % kLanes)) << 4));
+    uint16_t* dst = p.c + (m0 + r) * p.ldc + n0 + 8 * q;
+    if (p.ldc % 8 == 0) {
+      st_stream16(reinterpret_cast<uint4*>(dst), o);
+    } else {
+      st_stream8(reinterpret_cast<uint2*>(dst), o.x, o.y);
+      st_stream8(reinterpret_cast<uint2*>(dst + 4), o.z, o.w);
     }
   }
 }
