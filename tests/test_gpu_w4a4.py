@@ -205,6 +205,36 @@ def test_grouped_many_experts():
     _grouped(counts.tolist(), 32, 128, 5, tail=2)
 
 
+@pytest.mark.parametrize("K", [256, 1152])
+@pytest.mark.parametrize("per", [2, 20, 70])
+def test_grouped_wrong_offsets_and_rows(per, K):
+    """Offsets and rows out of range: nothing outside the S output rows is
+    written, and the experts whose own slots and rows are in range are right."""
+    E, N, Ma, S = 4, 48, 9, 4 * per
+    g = synth.rng(per + K)
+    a, ae = _operand(g, Ma, K)
+    w, we, pre, desc = _experts(g, E, N, K)
+    off = np.array([0, per, 2 * per, 2 * per, S + 1000000], np.int32)    # expert 3: clamped to S
+    rows = g.integers(0, Ma, S).astype(np.int32)
+    rows[per:2 * per] = g.choice([-7, -1, Ma, 1 << 30, -(1 << 31)], per)
+    buf = torch.full((S + 40, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    bs.bsgemm_w4a4_mxfp4_grouped(dev_u8(a), dev_u8(ae), torch.from_numpy(off).cuda(), desc, pre,
+                                 rows=torch.from_numpy(rows).cuda(), out=buf[20:20 + S])
+    torch.cuda.synchronize()
+    got = host_bits16(buf)
+    assert (got[:20] == 0x40E0).all() and (got[20 + S:] == 0x40E0).all()
+    got = got[20:20 + S]
+    for e, r in ((0, slice(0, per)), (3, slice(2 * per, S))):
+        ce, asum = mxfp4.w4a4_gemm(a[rows[r]], ae[rows[r]], w[e], we[e])
+        mxfp4.assert_w4a4_close(got[r], ce, asum, K, f"expert {e}")
+    off[:] = [S + 5, -3, per, 0, -(1 << 31)]                              # decreasing, negative
+    bs.bsgemm_w4a4_mxfp4_grouped(dev_u8(a), dev_u8(ae), torch.from_numpy(off).cuda(), desc, pre,
+                                 rows=torch.from_numpy(rows).cuda(), out=buf[20:20 + S])
+    torch.cuda.synchronize()
+    got = host_bits16(buf)
+    assert (got[:20] == 0x40E0).all() and (got[20 + S:] == 0x40E0).all()
+
+
 def test_grouped_no_slots():
     g = synth.rng(1)
     _, _, pre, desc = _experts(g, 3, 16, 128)
