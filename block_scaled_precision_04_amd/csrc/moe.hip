@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int* __restrict
   int next = r.begin + l < r.end ? ids[r.begin + l] : -1;
   for (int p0 = r.begin; p0 < r.end; p0 += 64) {
     const int p = p0 + l, id = next;
-    next = p + 64 < r.end ? ids[p + 64] : -1;   // loaded under this round's ballots
+    next = p + 64 < r.end ? ids[p + 64] : -1;   // loaded under these ballots
     const bool keep = id >= 0 && id < E;
     unsigned long long same = __ballot(keep);
     for (int b = 0; b < id_bits; ++b) {
