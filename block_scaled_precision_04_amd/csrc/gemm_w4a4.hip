@@ -337,8 +337,8 @@ __global__ __launch_bounds__(TW * KW * 64) void k_w4a4_stream(W4A4Args p) {
 // through LDS in group order.  A step is a chain (barrier, LDS reads, MFMAs)
 // that one small wave tile per SIMD cannot hide; a second chain on the same
 // SIMD does, where splitting K over workgroups would send every partial tile
-// through memory (M = 65 N = K = 5120: 64 x 128 tiles with two groups 9.3 us,
-// 128 x 128 tiles with K split over workgroups 12.9).
+// through memory (M = 65 N = K = 5120: 9.3 us, 128 x 128 tiles with K split over
+// workgroups 12.9).
 //
 // AS16: the activation scale rows are 16-byte aligned and K is a multiple of
 // 512, so a row's window is one 16-byte load (rows of 16 B); otherwise it is
@@ -813,24 +813,28 @@ int launch_tile(const W4A4Args& p, int64_t wgs, hipStream_t st) {
 // The dense tile shapes and what a launch of each takes, in us: with x = tiles
 // / 256 (one per CU) and R = ceil(x) rounds,
 //   t = start + R * (round + steps * step) + x * steps * load
-// least squares over 13 row counts from 24 to 4096 at eight N x K, N = 1024 ..
-// 17408 and K = 1024 .. 17408, weights pooled past the last-level cache (rms 10
-// to 14%, less where a shape is near the best; the shape with the smallest t is
-// the measured best or within 1% of it in 100 of the 104, at worst 7%).  128 x
-// 256, whose two workgroups fill a CU's LDS, takes over between half a round
-// and one of the large tiles (M = 1024 N = K = 5120 29.1 us, 128 x 128 36.8, 256
-// x 256 41.0).  With exactly 256 workgroups of it some CUs get two and others
-// none (M = 2048 N = 4096 K = 1024 15.2 us; 192 of them 8.9): two rounds.
+// fitted over 13 row counts from 24 to 4096 at ten N x K, N = 1024 .. 17408 and
+// K = 512 .. 17408, weights pooled past the last-level cache: by least squares
+// (rms 12 to 18%), then moved to the least loss by the choice (the shape with
+// the smallest t is the measured best or within 1% of it in 124 of the 130, at
+// worst 14%).  128 x 256, whose two workgroups fill a CU's LDS, takes over
+// between half a round and one of the large tiles (M = 1024 N = K = 5120 28.2
+// us, 128 x 128 36.8, 256 x 256 41.0); with exactly 256 workgroups of it some
+// CUs may get two and others none (M = 2048 N = 4096 K = 1024 9.0 to 15.2 us;
+// 192 of them 8.9): two rounds.  Two K groups of 64 x 64 tiles pay from K =
+// 2048 on (M = 24 N = K = 5120 9.3 us, one group 11.3; N = 4096 K = 1024 4.0
+// and 3.8), of 64 x 128 tiles nowhere (M = 128 N = 10240 K = 5120 17.1, one 16.5).
 struct TileShape {
   int bm, bn;
   float start, round, step, load;
 };
 constexpr TileShape kTiles[] = {
-    {256, 256, 0.90f, 6.98f, 0.512f, 0.517f}, // 4 waves of 128 x 128
-    {128, 256, 3.71f, 0.38f, 0.385f, 0.286f}, // 4 waves of 64 x 128, two workgroups a CU
-    {128, 128, 2.36f, 0.43f, 0.283f, 0.159f}, // 4 waves of 64 x 64, two workgroups a CU
-    {64, 128, 1.58f, 1.67f, 0.188f, 0.116f},  // 2 K groups of 4 waves of 64 x 32
-    {64, 64, 2.42f, 0.30f, 0.134f, 0.060f},   // 2 K groups of 2 waves of 64 x 32, two workgroups a CU
+    {256, 256, 0.362f, 7.182f, 0.420f, 0.617f}, // 4 waves of 128 x 128
+    {128, 256, 2.993f, 0.687f, 0.388f, 0.270f}, // 4 waves of 64 x 128, two workgroups a CU
+    {128, 128, 2.326f, 0.716f, 0.265f, 0.160f}, // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 3.186f, 0.181f, 0.243f, 0.037f},  // 4 waves of 64 x 32, three workgroups a CU
+    {64, 64, 2.547f, 0.465f, 0.125f, 0.056f},   // 2 K groups of 2 waves of 64 x 32, two workgroups a CU
+    {64, 64, 2.425f, 0.000f, 0.207f, 0.010f},   // 4 waves of 32 x 32, four workgroups a CU
 };
 float tile_cost(int i, int M, int N, int KS) {
   const TileShape& t = kTiles[i];
@@ -841,7 +845,7 @@ float tile_cost(int i, int M, int N, int KS) {
 }
 int best_tile(int M, int N, int KS) {
   int best = 0;
-  for (int i = 1; i < 5; ++i)
+  for (int i = 1; i < 6; ++i)
     if (tile_cost(i, M, N, KS) < tile_cost(best, M, N, KS)) best = i;
   return best;
 }
@@ -860,8 +864,9 @@ int run_tiles(int i, const W4A4Args& q, int n0, int n1, hipStream_t st) {
     case 0: return launch_tile<256, 256, 2, 2, 1, 4, 1, false>(p, wgs, st);
     case 1: return launch_tile<128, 256, 2, 2, 1, 3, 2, false>(p, wgs, st);
     case 2: return launch_tile<128, 128, 2, 2, 1, 4, 2, false>(p, wgs, st);
-    case 3: return launch_tile<64, 128, 1, 4, 2, 4, 2, false>(p, wgs, st);
-    default: return launch_tile<64, 64, 1, 2, 2, 4, 2, false>(p, wgs, st);
+    case 3: return launch_tile<64, 128, 1, 4, 1, 4, 3, false>(p, wgs, st);
+    case 4: return launch_tile<64, 64, 1, 2, 2, 4, 2, false>(p, wgs, st);
+    default: return launch_tile<64, 64, 2, 2, 1, 4, 4, false>(p, wgs, st);
   }
 }
 

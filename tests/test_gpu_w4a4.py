@@ -33,14 +33,14 @@ DENSE = [
     (16, 48, 5120), (16, 96, 12544), (2, 16, 5248), (9, 4112, 2304), (12, 8208, 2304), (3, 4112, 12416),
     # weight stream, 17 to 64 rows of long K
     (20, 48, 12416), (33, 48, 12288), (64, 80, 12544),
-    # 64 x 64 tiles
+    # 64 x 64 tiles: short K, longer K in two K groups
     (17, 160, 1152), (32, 256, 2048), (33, 144, 256), (64, 1040, 1280), (65, 16, 128), (65, 128, 1024),
     (100, 272, 2176), (128, 128, 128), (129, 400, 384), (300, 1296, 640), (513, 144, 8192), (200, 2064, 512),
     (1000, 528, 256), (65, 144, 12416), (65, 144, 12288), (70, 64, 16384),
     # 64 x 128 tiles
-    (513, 2064, 1024), (513, 2064, 896),
+    (513, 2064, 1024), (513, 2064, 896), (600, 2064, 4224), (300, 4112, 2048),
     # 128 x 128 tiles
-    (1100, 2064, 1024),
+    (1100, 2064, 1024), (1100, 2064, 1152),
     # 128 x 256 tiles
     (1000, 4112, 640), (900, 4112, 1024),
 ]
