@@ -938,10 +938,10 @@ int launch_grouped_stream(W4A4Args& p, int S, hipStream_t st) {
 //     against 34.8); 64 columns in four K groups where even that leaves half
 //     the CUs idle (8 rows of K = 2048 5.8 us against 7.1; 8 experts, one row of
 //     N = K = 4096 7.6 against 10.8);
-//   - up to 48 rows: 64 x 128 tiles, three workgroups a CU, whose loads run
-//     ahead over all of K (256 experts N = 1024 K = 2048, 16 rows 54 us, the
-//     stream 60; 32 rows 33 us from the cache, the tiles below 40);
-//   - above: 128 x 256 tiles, two workgroups a CU, so one's stores run under the
+//   - up to 32 rows of K > 1024: 64 x 128 tiles, three workgroups a CU (64
+//     experts N = 1024 K = 2048: 15 rows 16.1 us, 128 x 256 16.9; 37 rows 17.8 and
+//     17.4, 48 rows 21.4 and 17.6; 256 experts, 16 rows 54 us, the stream 60);
+//   - else 128 x 256 tiles, two workgroups a CU, so one's stores run under the
 //     other's MFMAs (256 experts N = 1024 K = 2048, 65536 rows 118 us; 128 x 128
 //     144, 256 x 256 142, which gains from 2000 rows of K = 7168 on only, 7%).
 int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int64_t lds, const int* offsets,
@@ -971,7 +971,7 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
     if (p.KS > 16 || (wgs <= 512 && p.KS > 4)) return launch_grouped_stream<4, 2, 2, 4>(p, S, st);
     return launch_grouped_stream<8, 1, 2, 4>(p, S, st);
   }
-  if (avg <= 48)
+  if (p.KS > 8 && avg <= 32)
     return launch_tile<64, 128, 1, 4, 1, 4, 3, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 127) / 128),
                                                      st);
   return launch_tile<128, 256, 2, 2, 1, 3, 2, true>(p, static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 255) / 256),

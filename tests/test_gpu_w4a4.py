@@ -187,6 +187,15 @@ def test_grouped_few_rows(E, N, K):
     _grouped(counts.tolist(), N, K, 5, tail=3, seed=1)
 
 
+@pytest.mark.parametrize("counts,N,K", [([20] * 6 + [64, 1], 272, 2048), ([25, 0, 31, 12], 144, 1664),
+                                        ([65, 0, 0, 1, 30, 33], 80, 4096), ([20] * 6 + [64, 1], 272, 512),
+                                        ([25, 17, 31, 12], 400, 896)])
+def test_grouped_some_rows(counts, N, K):
+    """Between 10 and 32 rows an expert: 64 x 128 tiles for long K, 128 x 256 for short."""
+    _grouped(counts, N, K, 50)
+    _grouped(counts, N, K, 50, tail=5, seed=1)
+
+
 @pytest.mark.parametrize("N,K", [(80, 256), (528, 384), (2048, 128)])
 def test_grouped_many_row_tiles(N, K):
     """Enough row tiles that runs of them go to one XCD, with a rest that does not."""
