@@ -681,8 +681,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
 
   // Epilogue: the tile through LDS as bf16, so that a row leaves as whole
   // 16-byte pieces side by side.  A lane's four columns are half a piece; piece
-  // q of a row sits at slot q ^ (row % pieces), which spreads a write's 32 rows
-  // over all banks.
+  // q of a row sits at slot q ^ (row % pieces), which leaves two rows of a write's
+  // 32 on a bank (their halves swapped on every other 16 rows would leave one, and
+  // is 1 to 2% slower: the reads have to swap them back).
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __syncthreads();       // the stages are done with
   constexpr int kLanes = BN / 8, kRows = C::kThreads * KG / kLanes;   // pieces of a row, rows at once
