@@ -414,7 +414,8 @@ BS_API int moe_sort(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* of
  * rows of xs that no pair names are left as they are.  x: bf16 [T, K]; xs:
  * bf16 [T * k, K]; dense, 16-byte aligned.  K % 8 == 0, K <= 32768,
  * T * k <= 2^24, T * K / 8 < 2^31 (here and below).  Entries of pos outside
- * [0, T * k) count as dropped.  Its gradient is moe_combine with weights NULL. */
+ * [0, T * k) count as dropped; a slot may be named once only, as moe_sort does.
+ * Its gradient is moe_combine with weights NULL. */
 BS_API int moe_gather(const void* x, const int32_t* pos, void* xs, int T, int k, int K, bs_stream_t stream);
 
 /* Expert rows back in token order: out[t, :] = bf16( sum_j weights[t, j] *
