@@ -97,9 +97,11 @@ __global__ __launch_bounds__(kQT) void k_quant_mxfp4(const uint16_t* __restrict_
 // interval h * (1 +- 2^-20) takes one code (and the block maximum's interval
 // one exponent); the hardware exp2 and reciprocal, with the rounding error of
 // g * log2(e) added back, stay within 5 fp32 ulps (6e-7 < 2^-20) for
-// 2^-100 <= |g| and g >= -87.  The few blocks where that does not decide --
-// about one in 10^4 of ordinary data, and those out of that range or near the
-// ends of fp32 -- are computed again in fp64.
+// 2^-100 <= |g| and -87 <= g < 2.35e38.  The few blocks where that does not
+// decide -- about one in 10^4 of ordinary data, and those out of that range or
+// near the ends of fp32 -- are computed again in fp64.  (From 2.36e38 on
+// g * log2(e) overflows and the approximate h is a NaN whatever u is, a zero too,
+// so a maximum that is not finite always asks for it.)
 constexpr float kEps = 0x1p-20f;
 
 template <int U>
@@ -143,7 +145,7 @@ __global__ __launch_bounds__(kQT) void k_silu_quant_mxfp4(const uint4* __restric
     const float am = __uint_as_float(amax);
     uint32_t byte = e8m0_of(__float_as_uint(am * (1.0f - kEps)));
     redo |= e8m0_of(__float_as_uint(am * (1.0f + kEps))) != byte;
-    redo |= live && !(am >= 0x1p-100f && am < 0x1p126f);
+    redo |= !(am < 0x1p126f) || (live && am < 0x1p-100f);
     uint32_t w;
     {
       const float inv = inv_scale(byte);
