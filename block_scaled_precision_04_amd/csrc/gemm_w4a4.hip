@@ -720,13 +720,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w4a4_tile(W4A4Args p
 
 // ---------------------------------------------------------------- host side
 constexpr size_t kMaxStreamLds = 160 * 1024 - 256;
-
-// The weight stream takes up to 16 rows (M = 16 N = K = 5120 6.3 us, tiles 8.9),
-// and up to 64 where K is long and N narrow (K >= 12288, N < 8192): there its K
-// splits over workgroups keep more of the GPU loading than the tiles' K groups
-// (M = 48: N = 5120 K = 17408 24.4 us against 28.5; N = 7168 K = 12288 22.0
-// against 21.6).
-bool use_stream(int M, int N, int KS) { return M <= 16 || (M <= 64 && KS >= 96 && N < 8192); }
+constexpr int kMaxSplits = 65535;   // grid z
 
 struct StreamCfg {
   int mb, tw, kw, t, r, rs, groups, mtiles, s, iters;
@@ -764,10 +758,24 @@ StreamCfg dense_stream_cfg(int M, int N, int KS) {
   return d;
 }
 
+// The weight stream takes up to 16 rows (M = 16 N = K = 5120 6.3 us, tiles 8.9),
+// and up to 64 where K is long and N narrow (K >= 12288, N < 8192): there its K
+// splits over workgroups keep more of the GPU loading than the tiles' K groups
+// (M = 48: N = 5120 K = 17408 24.4 us against 28.5; N = 7168 K = 12288, the
+// border, 22.0 against 21.6).  A split has a counter for every column group and
+// a grid layer for every run of K: wider N (from 786448 at K > 5120) and longer
+// K (past 67 million, up to 16 rows 335 million) are left to the tiles, which
+// need neither.
+bool use_stream(int M, int N, int KS) {
+  if (M > 16 && (M > 64 || KS < 96 || N >= 8192)) return false;
+  const StreamCfg d = dense_stream_cfg(M, N, KS);
+  return d.s == 1 || (d.s <= kMaxSplits && d.groups * d.mtiles <= kWsMaxCounters);
+}
+
 template <int MB, int TW, int KW, int T, int R, bool GROUPED>
 int launch_stream(const StreamCfg& d, W4A4Args& p, hipStream_t st) {
   const size_t lds = stream_lds(d);
-  if (lds > kMaxStreamLds || d.mtiles > 65535 || d.s > 65535) return BS_ERR_SHAPE;
+  if (lds > kMaxStreamLds || d.mtiles > 65535 || d.s > kMaxSplits) return BS_ERR_SHAPE;
   p.rs = d.rs;
   p.iters = d.iters;
   auto* fn = &k_w4a4_stream<MB, TW, KW, T, R, GROUPED>;
@@ -782,7 +790,6 @@ int launch_stream(const StreamCfg& d, W4A4Args& p, hipStream_t st) {
 int run_dense_stream(W4A4Args& p, void* ws, hipStream_t st) {
   const StreamCfg d = dense_stream_cfg(p.M, p.N, p.KS);
   if (d.s > 1) {
-    if (d.groups * d.mtiles > kWsMaxCounters) return BS_ERR_SHAPE;
     p.counters = static_cast<int*>(ws);
     p.slab = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
   }

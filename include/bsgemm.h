@@ -139,7 +139,8 @@ BS_API int bs_unprelayout_mxfp4(const bs_wdesc* desc, const void* pre, void* w_p
  * shapes, whose bs_workspace_bytes it covers.  Calls that share a workspace
  * must be ordered (same stream); 0 means no workspace is needed.  A split
  * that would need more than 16384 counters (one per 16-column tile group)
- * is refused with BS_ERR_SHAPE.
+ * is refused with BS_ERR_SHAPE; the W4A4 GEMM does not split there and needs
+ * no workspace.
  * Memory kind: ordinary device memory of the GPU the call runs on (hipMalloc,
  * coarse-grained).  The workgroups of one tile may run on different XCDs,
  * whose L2 caches are not coherent with each other; the hand-off works
