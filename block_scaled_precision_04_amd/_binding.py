@@ -141,9 +141,10 @@ def _need(cond, fn, msg):
         raise ValueError(f"{fn}: {msg}")
 
 
-def _arg(fn, name, t, shape, dtypes, contiguous=False, unit_inner=True):
+def _arg(fn, name, t, shape, dtypes, contiguous=False, unit_inner=True, one_row=False):
     """t must have `shape` and one of `dtypes`; its last dimension must be
-    unit-stride (rows may be padded) or, with contiguous=True, the tensor dense."""
+    unit-stride (rows may be padded) or, with contiguous=True, the tensor dense.
+    one_row=True: a single row may have any row stride (the caller passes a dense one on)."""
     # an accepted tensor builds no message: formatting one for every argument
     # took most of a small call's host time
     if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape):
@@ -151,13 +152,15 @@ def _arg(fn, name, t, shape, dtypes, contiguous=False, unit_inner=True):
         _need(isinstance(t, torch.Tensor), fn, f"{name} must be a torch.Tensor")
         _need(t.dtype in dtypes, fn, f"{name} has dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
         _need(tuple(t.shape) == tuple(shape), fn, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return t
     if contiguous:
-        _need(False, fn, f"{name} must be contiguous")
-    elif unit_inner and t.dim() >= 2 and t.shape[-1] > 1:
-        _need(t.stride(-1) == 1, fn, f"{name} must have unit stride along its last dimension")
-        _need(t.stride(0) >= t.shape[-1], fn, f"{name} rows overlap (stride {t.stride(0)} < {t.shape[-1]})")
+        if not t.is_contiguous():
+            _need(False, fn, f"{name} must be contiguous")
+    elif unit_inner and t.dim() >= 2 and t.shape[-1] > 1 and not (one_row and t.is_contiguous()):
+        # (is_contiguous() looks at no stride of a dimension of one)
+        if t.stride(-1) != 1:
+            _need(False, fn, f"{name} must have unit stride along its last dimension")
+        if t.stride(0) < t.shape[-1]:
+            _need(False, fn, f"{name} rows overlap (stride {t.stride(0)} < {t.shape[-1]})")
     return t
 
 
@@ -379,8 +382,8 @@ def _mxfp4_activation(fn, a, a_scale, desc):
     K = 2 * Kh
     if desc.K != K:
         _need(False, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
-    _arg(fn, "a", a, (M, Kh), _U8)
-    _arg(fn, "a_scale", a_scale, (M, K // 32), _U8)
+    _arg(fn, "a", a, (M, Kh), _U8, one_row=True)
+    _arg(fn, "a_scale", a_scale, (M, K // 32), _U8, one_row=True)
     return M, K
 
 
@@ -399,7 +402,7 @@ def bsgemm_w4a4_mxfp4(a, a_scale, desc, w_pre, out=None, ws=None):
     if out is None:
         out = _rows(M, N, torch.bfloat16, a.device)
     else:
-        _arg(fn, "out", out, (M, N), _BF16)
+        _arg(fn, "out", out, (M, N), _BF16, one_row=True)
     stream = _on_current(fn, a, a_scale, w_pre, out, ws)
     ws_p, ws_n = _ws(fn, ws)
     # (with one row any stride is a dense one)
@@ -421,7 +424,7 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
     N = desc.N
     _need(isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
     E = w_pre.shape[0]
-    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), _U8)
+    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), _U8, one_row=True)
     if w_pre.shape[1] < desc.total_bytes:
         _need(False, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs {desc.total_bytes}")
     _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
@@ -433,7 +436,7 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
     if out is None:
         out = _rows(S, N, torch.bfloat16, a.device)
     else:
-        _arg(fn, "out", out, (S, N), _BF16)
+        _arg(fn, "out", out, (S, N), _BF16, one_row=True)
     stream = _on_current(fn, a, a_scale, offsets, w_pre, rows, out)
     _check(fn, lib().bsgemm_w4a4_mxfp4_grouped(
         a.data_ptr(), _row_stride(a), a_scale.data_ptr(), _row_stride(a_scale), Ma, offsets.data_ptr(), _ptr(rows),
