@@ -9,15 +9,16 @@
 // is the pre-laid-out MXFP4 weight of the W4A8 GEMM.
 //
 // Two kernels.  Few rows: a weight stream (k_w4a4_stream), bound by HBM (M = 8
-// N = 17408 K = 5120: 9.9 us, 4.8 TB/s, where a large copy runs at 5.2).  Many
-// rows: LDS-tiled (k_w4a4_tile), fed through direct-to-LDS loads and bound by
-// the matrix cores' power: M = 8192 N = 10240 K = 5120 takes 196 to 213 us by
-// card (4.0 to 4.4 PFLOP/s), 154 us when every code is zero, and 178 us with all
-// loads and LDS reads taken out of the loop.  Both have a grouped form: the slots of the
-// sorted (token, expert) pairs are cut into row tiles expert by expert, and
-// every workgroup finds its tile from the expert offsets on the device, so the
-// host never waits for them; the activation rows are read through the sorted
-// order (row gather in the loads), never copied.
+// N = 17408 K = 5120: 11.1 to 11.7 us with the weight from HBM, 4.1 to 4.3 TB/s,
+// where a large copy runs at 5.2; 9.9 from the last-level cache).  Many rows:
+// LDS-tiled (k_w4a4_tile), fed through direct-to-LDS loads and bound by the matrix
+// cores' power: M = 8192 N = 10240 K = 5120 takes 196 to 213 us by card (4.0 to
+// 4.4 PFLOP/s), 154 us when every code is zero, and 178 us with all loads and LDS
+// reads taken out of the loop.  Both have a grouped form: the slots of the sorted
+// (token, expert) pairs are cut into row tiles expert by expert, and every
+// workgroup finds its tile from the expert offsets on the device, so the host
+// never waits for them; the activation rows are read through the sorted order
+// (row gather in the loads), never copied.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -269,9 +269,10 @@ BS_API int gemm_bf16_skinny_noalloc(const void* x, const void* w, void* c, int M
  * c: bf16 [M, N] (ldc elements, multiple of 4).  Needs 1 <= M <= 2^22,
  * N % 16 == 0, K % 128 == 0; a, c 16-byte, a_scale 4-byte, w_pre 256-byte
  * aligned; M * lda, M * ld_scale and N * K / 2 < 2^32.
- * Few rows (at most 64) run a weight stream, more an LDS-tiled kernel; the
- * stream may split K through ws of bs_workspace_bytes(BS_OP_W4A4_MXFP4, M, N,
- * K) bytes (256-byte aligned, zeroed once); when that is 0, ws may be NULL. */
+ * Up to 16 rows (up to 64 where K >= 12288 and N < 8192) run a weight stream,
+ * others an LDS-tiled kernel; the stream may split K through ws of
+ * bs_workspace_bytes(BS_OP_W4A4_MXFP4, M, N, K) bytes (256-byte aligned, zeroed
+ * once); when that is 0, ws may be NULL. */
 BS_API int bsgemm_w4a4_mxfp4(const void* a, int64_t lda, const void* a_scale, int64_t ld_scale, const bs_wdesc* wd,
                              const void* w_pre, void* c, int64_t ldc, int M, int N, int K, void* ws, size_t ws_bytes,
                              bs_stream_t stream);
