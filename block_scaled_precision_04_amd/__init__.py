@@ -12,8 +12,11 @@ _BINDING_NAMES = (
     "add_rms_quant_fp8", "add_rms_quant_fp8_group128", "silu_mul_quant_fp8", "quant_fp8_per_token", "quant_fp8_group128", "quant_fp8_block128",
     "prelayout_mxfp4_experts", "bsgemm_w4a4_mxfp4", "bsgemm_w4a4_mxfp4_grouped", "quant_mxfp4",
     "silu_mul_quant_mxfp4", "dequant_mxfp4", "moe_sort", "moe_gather", "moe_combine", "moe_combine_backward",
+    "prelayout_int8", "prelayout_int8_experts", "unprelayout_int8", "bsgemm_w8a8_int8", "bsgemm_w8a8_int8_grouped",
+    "quant_int8_per_token", "add_rms_quant_int8", "silu_mul_quant_int8", "dequant_int8", "moe_route",
+    "moe_route_backward",
     "BsError", "WDesc", "lib", "BS_OP_FP8_BLOCK", "BS_OP_W4A8_MXFP4", "BS_OP_BF16_SKINNY", "BS_OP_W4A4_MXFP4",
-    "BS_OP_MOE_SORT",
+    "BS_OP_MOE_SORT", "BS_OP_W8A8_INT8", "BS_TYPE_F32", "BS_TYPE_BF16", "BS_SCORE_SOFTMAX", "BS_SCORE_SIGMOID",
 )
 
 

@@ -20,8 +20,14 @@ BS_OP_W4A8_MXFP4 = 2
 BS_OP_BF16_SKINNY = 3
 BS_OP_W4A4_MXFP4 = 4
 BS_OP_MOE_SORT = 5
+BS_OP_W8A8_INT8 = 6
+BS_TYPE_F32 = 0
+BS_TYPE_BF16 = 1
+BS_SCORE_SOFTMAX = 0
+BS_SCORE_SIGMOID = 1
 BS_LAYOUT_FP8_BLOCK = 0x38423631
 BS_LAYOUT_MXFP4 = 0x34584D31
+BS_LAYOUT_INT8 = 0x38544E49
 BS_WDESC_MAGIC = 0x42534744
 
 
@@ -73,6 +79,17 @@ SIGNATURES = {
     "quant_mxfp4": (_I, [_P, _L, _P, _P, _I, _I, _P]),
     "silu_mul_quant_mxfp4": (_I, [_P, _P, _P, _P, _I, _I, _P]),
     "dequant_mxfp4": (_I, [_P, _P, _P, _I, _I, _P]),
+    "bs_prelayout_int8_bytes": (_Z, [_I, _I]),
+    "bs_prelayout_int8": (_I, [_P, _P, _Z, _I, _I, _D, _P]),
+    "bs_unprelayout_int8": (_I, [_D, _P, _P, _P]),
+    "bsgemm_w8a8_int8": (_I, [_P, _L, _P, _D, _P, _P, _P, _L, _I, _I, _I, _P, _Z, _P]),
+    "bsgemm_w8a8_int8_grouped": (_I, [_P, _L, _P, _I, _P, _P, _D, _P, _Z, _P, _P, _L, _I, _I, _I, _I, _P]),
+    "quant_int8_per_token": (_I, [_P, _L, _P, _P, _I, _I, _P]),
+    "add_rms_quant_int8": (_I, [_P, _P, _P, _F, _F, _P, _P, _P, _I, _I, _P]),
+    "silu_mul_quant_int8": (_I, [_P, _P, _P, _P, _I, _I, _P]),
+    "dequant_int8": (_I, [_P, _P, _P, _I, _I, _P]),
+    "moe_route": (_I, [_P, _L, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P, _I, _I, _I, _P]),
+    "moe_route_backward": (_I, [_P, _P, _L, _I, _P, _I, _I, _F, _P, _L, _I, _I, _I, _P]),
     "moe_sort": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _Z, _P]),
     "moe_gather": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "moe_combine": (_I, [_P, _P, _P, _P, _I, _I, _I, _P]),
@@ -134,6 +151,7 @@ _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _U8 = (torch.uint8,)
 _I32 = (torch.int32,)
 _F32 = (torch.float32,)
+_I8 = (torch.int8,)
 
 
 def _need(cond, fn, msg):
@@ -210,6 +228,11 @@ def _ws(fn, ws):
     return _ptr(ws), ws.numel() * ws.element_size()
 
 
+def _aligned(t):
+    """t dense and 16-byte aligned (itself where it is)."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 def _bits16(t):
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return t
@@ -283,6 +306,45 @@ def unprelayout_mxfp4(desc, pre):
     _check("bs_unprelayout_mxfp4", lib().bs_unprelayout_mxfp4(ctypes.byref(desc), _ptr(pre), _ptr(wp), _ptr(e),
                                                                _stream()))
     return wp, e
+
+
+def prelayout_int8(w):
+    """[N, K] int8 -> (pre-laid-out uint8 buffer, WDesc).  K % 16 == 0, K < 2^17."""
+    fn = "prelayout_int8"
+    _need(isinstance(w, torch.Tensor) and w.dim() == 2, fn, "w must be a 2-D tensor [N, K]")
+    out, desc = prelayout_int8_experts(w[None], fn)
+    return out[0], desc
+
+
+def prelayout_int8_experts(w, fn="prelayout_int8_experts"):
+    """[E, N, K] int8 -> (uint8 [E, total_bytes] with every expert's pre-laid-out
+    weight, the WDesc that they share)."""
+    _need(isinstance(w, torch.Tensor) and w.dim() == 3, fn, "w must be a 3-D tensor [E, N, K]")
+    E, N, K = w.shape
+    _need(E >= 1, fn, "at least one expert is needed")
+    _arg(fn, "w", w, (E, N, K), _I8, unit_inner=False)
+    nbytes = lib().bs_prelayout_int8_bytes(N, K)
+    if nbytes == 0:
+        raise BsError("bs_prelayout_int8_bytes", -2)
+    stream = _on_current(fn, w)
+    out = torch.empty((E, nbytes), dtype=torch.uint8, device=w.device)
+    desc = WDesc()
+    for e in range(E):
+        we = _aligned(w[e])
+        _check(fn, lib().bs_prelayout_int8(we.data_ptr(), out[e].data_ptr(), nbytes, N, K, ctypes.byref(desc), stream))
+    return out, desc
+
+
+def unprelayout_int8(desc, pre):
+    """The int8 weight [N, K] that a pre-laid-out buffer holds."""
+    fn = "unprelayout_int8"
+    _need(isinstance(pre, torch.Tensor), fn, "pre must be a torch.Tensor")
+    _arg(fn, "pre", pre, (pre.numel(),), _U8, contiguous=True)
+    _need(pre.numel() >= desc.total_bytes, fn, f"pre holds {pre.numel()} bytes, the layout needs {desc.total_bytes}")
+    stream = _on_current(fn, pre)
+    w = _rows(desc.N, desc.K, torch.int8, pre.device)
+    _check(fn, lib().bs_unprelayout_int8(ctypes.byref(desc), pre.data_ptr(), w.data_ptr(), stream))
+    return w
 
 
 def workspace_bytes(op, M, N, K):
@@ -441,6 +503,74 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
     _check(fn, lib().bsgemm_w4a4_mxfp4_grouped(
         a.data_ptr(), _row_stride(a), a_scale.data_ptr(), _row_stride(a_scale), Ma, offsets.data_ptr(), _ptr(rows),
         ctypes.byref(desc), w_pre.data_ptr(), _row_stride(w_pre), out.data_ptr(), _row_stride(out), S, E, N, K, stream))
+    return out
+
+
+def _int8_activation(fn, a, a_scale, desc):
+    """Checked (rows, K) of an int8 activation: codes [M, K], scales [M]."""
+    _need(isinstance(a, torch.Tensor) and a.dim() == 2, fn, "a must be a 2-D tensor [M, K]")
+    M, K = a.shape
+    if desc.K != K:
+        _need(False, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
+    _arg(fn, "a", a, (M, K), _I8, one_row=True)
+    _arg(fn, "a_scale", a_scale, (M,), _F32, contiguous=True)
+    return M, K
+
+
+def bsgemm_w8a8_int8(a, a_scale, desc, w_pre, w_scale, out=None, ws=None):
+    """C[M,N] bf16 = int8 GEMM.  a: int8 [M, K] (row stride may be padded to a
+    multiple of 16); a_scale: fp32 [M]; desc, w_pre: from prelayout_int8;
+    w_scale: fp32 [N]; ws: alloc_workspace(BS_OP_W8A8_INT8, M, N, K)."""
+    fn = "bsgemm_w8a8_int8"
+    M, K = _int8_activation(fn, a, a_scale, desc)
+    N = desc.N
+    _need(isinstance(w_pre, torch.Tensor), fn, "w_pre must be a torch.Tensor")
+    nw = w_pre.numel()
+    _arg(fn, "w_pre", w_pre, (nw,), _U8, contiguous=True)
+    if nw < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {nw} bytes, the layout needs {desc.total_bytes}")
+    _arg(fn, "w_scale", w_scale, (N,), _F32, contiguous=True)
+    if out is None:
+        out = _rows(M, N, torch.bfloat16, a.device)
+    else:
+        _arg(fn, "out", out, (M, N), _BF16, one_row=True)
+    stream = _on_current(fn, a, a_scale, w_pre, w_scale, out, ws)
+    ws_p, ws_n = _ws(fn, ws)
+    _check(fn, lib().bsgemm_w8a8_int8(
+        a.data_ptr(), _row_stride(a), a_scale.data_ptr(), ctypes.byref(desc), w_pre.data_ptr(), w_scale.data_ptr(),
+        out.data_ptr(), _row_stride(out), M, N, K, ws_p, ws_n, stream))
+    return out
+
+
+def bsgemm_w8a8_int8_grouped(a, a_scale, offsets, desc, w_pre, w_scale, rows=None, out=None):
+    """The experts' int8 products over slots sorted by expert (moe_sort):
+    out[s] = a[rows[s]] . W_e^T for offsets[e] <= s < offsets[e+1]; bf16 [S, N].
+    offsets: int32 [E+1]; rows: int32 [S] (None: slot s is row s of a); desc,
+    w_pre: from prelayout_int8_experts; w_scale: fp32 [E, N].  Rows of out past
+    offsets[E] keep what they hold (pass out to choose; a fresh one is not cleared)."""
+    fn = "bsgemm_w8a8_int8_grouped"
+    Ma, K = _int8_activation(fn, a, a_scale, desc)
+    N = desc.N
+    _need(isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
+    E = w_pre.shape[0]
+    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), _U8, one_row=True)
+    if w_pre.shape[1] < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs {desc.total_bytes}")
+    _arg(fn, "w_scale", w_scale, (E, N), _F32, contiguous=True)
+    _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
+    S = Ma
+    if rows is not None:
+        _need(isinstance(rows, torch.Tensor), fn, "rows must be a torch.Tensor")
+        S = rows.numel()
+        _arg(fn, "rows", rows, (S,), _I32, contiguous=True)
+    if out is None:
+        out = _rows(S, N, torch.bfloat16, a.device)
+    else:
+        _arg(fn, "out", out, (S, N), _BF16, one_row=True)
+    stream = _on_current(fn, a, a_scale, offsets, w_pre, w_scale, rows, out)
+    _check(fn, lib().bsgemm_w8a8_int8_grouped(
+        a.data_ptr(), _row_stride(a), a_scale.data_ptr(), Ma, offsets.data_ptr(), _ptr(rows), ctypes.byref(desc),
+        w_pre.data_ptr(), _row_stride(w_pre), w_scale.data_ptr(), out.data_ptr(), _row_stride(out), S, E, N, K, stream))
     return out
 
 
@@ -666,7 +796,163 @@ def dequant_mxfp4(q, scale, out=None):
     return out
 
 
+# ------------------------------------------------------------------ int8 quantizers
+def _int8_out(fn, q, scale, M, K, device):
+    if q is None:
+        q = _rows(M, K, torch.int8, device)
+    else:
+        _arg(fn, "q", q, (M, K), _I8, contiguous=True)
+    if scale is None:
+        scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=device)
+    else:
+        _arg(fn, "scale", scale, (M,), _F32, contiguous=True)
+    return q, scale
+
+
+def quant_int8_per_token(x, q=None, scale=None):
+    """x bf16 [M, K] (row stride may be padded to a multiple of 8) -> (q int8 [M, K],
+    scale fp32 [M]); on a weight [N, K] the codes for prelayout_int8 and w_scale."""
+    fn = "quant_int8_per_token"
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [M, K]")
+    M, K = x.shape
+    _arg(fn, "x", x, (M, K), _BF16, unit_inner=False)
+    q, scale = _int8_out(fn, q, scale, M, K, x.device)
+    stream = _on_current(fn, x, q, scale)
+    ldx, inner = x.stride()
+    if M == 1:
+        ldx = K
+    if inner != 1 or ldx < K or ldx % 8 or x.data_ptr() % 16:
+        x, ldx = x.clone(memory_format=torch.contiguous_format), K
+    _check(fn, lib().quant_int8_per_token(x.data_ptr(), ldx, q.data_ptr(), scale.data_ptr(), M, K, stream))
+    return q, scale
+
+
+def add_rms_quant_int8(y, residual, gamma, eps=1e-6, offset=1.0, q=None, scale=None, residual_out=None):
+    """(q int8 [M,K], scale fp32 [M], residual_out bf16 [M,K]) of the norm of
+    y + residual with the weight offset + gamma.  residual None: the norm of y
+    (residual_out then comes back as it was given)."""
+    fn = "add_rms_quant_int8"
+    _need(isinstance(y, torch.Tensor) and y.dim() == 2, fn, "y must be a 2-D tensor [M, K]")
+    M, K = y.shape
+    _arg(fn, "y", y, (M, K), _BF16, unit_inner=False)
+    _arg(fn, "gamma", gamma, (K,), _BF16, unit_inner=False)
+    if residual is not None:
+        _arg(fn, "residual", residual, (M, K), _BF16, unit_inner=False)
+        if residual_out is None:
+            residual_out = _rows(M, K, torch.bfloat16, y.device)
+    if residual_out is not None:
+        _arg(fn, "residual_out", residual_out, (M, K), _BF16, contiguous=True)
+    q, scale = _int8_out(fn, q, scale, M, K, y.device)
+    stream = _on_current(fn, y, residual, gamma, q, scale, residual_out)
+    y, gamma = _aligned(y), _aligned(gamma)
+    if residual is not None:
+        residual = _aligned(residual)
+    _check(fn, lib().add_rms_quant_int8(y.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, offset, q.data_ptr(),
+                                        scale.data_ptr(), _ptr(residual_out), M, K, stream))
+    return q, scale, residual_out
+
+
+def silu_mul_quant_int8(gu, q=None, scale=None, rows=None):
+    """gu bf16 [M, 2N] (gate half first) -> (q int8 [M, N], scale fp32 [M]) of
+    silu(gate) * up.  rows: optional int32 tensor of one element; only the first
+    min(rows, M) rows are computed (e.g. offsets[E:])."""
+    fn = "silu_mul_quant_int8"
+    _need(isinstance(gu, torch.Tensor) and gu.dim() == 2 and gu.shape[1] % 2 == 0, fn,
+          "gu must be a 2-D tensor [M, 2N]")
+    M, N = gu.shape[0], gu.shape[1] // 2
+    _arg(fn, "gu", gu, (M, 2 * N), _BF16, unit_inner=False)
+    if rows is not None:
+        _arg(fn, "rows", rows, (1,), _I32)
+    q, scale = _int8_out(fn, q, scale, M, N, gu.device)
+    stream = _on_current(fn, gu, q, scale, rows)
+    gu = _aligned(gu)
+    _check(fn, lib().silu_mul_quant_int8(gu.data_ptr(), q.data_ptr(), scale.data_ptr(), _ptr(rows), M, N, stream))
+    return q, scale
+
+
+def dequant_int8(q, scale, out=None):
+    """(q int8 [M, K], scale fp32 [M]) -> the values, bf16 [M, K]."""
+    fn = "dequant_int8"
+    _need(isinstance(q, torch.Tensor) and q.dim() == 2, fn, "q must be a 2-D tensor [M, K]")
+    M, K = q.shape
+    _arg(fn, "q", q, (M, K), _I8, unit_inner=False)
+    _arg(fn, "scale", scale, (M,), _F32, contiguous=True)
+    if out is None:
+        out = _rows(M, K, torch.bfloat16, q.device)
+    else:
+        _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
+    stream = _on_current(fn, q, scale, out)
+    q = _aligned(q)
+    _check(fn, lib().dequant_int8(q.data_ptr(), scale.data_ptr(), out.data_ptr(), M, K, stream))
+    return out
+
+
 # ------------------------------------------------------------------ mixture of experts
+_LOGITS = {torch.float32: BS_TYPE_F32, torch.bfloat16: BS_TYPE_BF16}
+
+
+def _moe_logits(fn, name, x, shape):
+    """Checked (type, row stride) of logits [T, E]."""
+    _arg(fn, name, x, shape, tuple(_LOGITS), one_row=True)
+    return _LOGITS[x.dtype], _row_stride(x)
+
+
+def moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, groups=1, topk_groups=1, group_top=1, renorm=True,
+              scale=1.0, rows=None, ids=None, weights=None):
+    """The k experts of each token and their weights from logits [T, E] (fp32 or
+    bf16, rows may be padded): (ids int32 [T, k], -1 where no expert is left;
+    weights fp32 [T, k]).  score: BS_SCORE_SOFTMAX or BS_SCORE_SIGMOID; bias: fp32
+    [E], added for the choice only; groups, topk_groups, group_top: the choice is
+    within the topk_groups runs of E / groups experts whose group_top largest sum
+    highest; renorm: weights divided by their sum; all times scale.  rows:
+    optional int32 tensor of one element, tokens from it on are padding.
+    ids and weights go to moe_sort and moe_combine."""
+    fn = "moe_route"
+    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2, fn, "logits must be a 2-D tensor [T, E]")
+    T, E = logits.shape
+    type_, ld = _moe_logits(fn, "logits", logits, (T, E))
+    for name, v in (("k", k), ("groups", groups), ("topk_groups", topk_groups), ("group_top", group_top)):
+        if not (isinstance(v, int) and v >= 1):
+            _need(False, fn, f"{name} = {v!r} must be a positive int")
+    if bias is not None:
+        _arg(fn, "bias", bias, (E,), _F32, contiguous=True)
+    if rows is not None:
+        _arg(fn, "rows", rows, (1,), _I32)
+    if ids is None:
+        ids = _rows(T, k, torch.int32, logits.device)
+    else:
+        _arg(fn, "ids", ids, (T, k), _I32, contiguous=True)
+    if weights is None:
+        weights = _rows(T, k, torch.float32, logits.device)
+    else:
+        _arg(fn, "weights", weights, (T, k), _F32, contiguous=True)
+    stream = _on_current(fn, logits, bias, rows, ids, weights)
+    _check(fn, lib().moe_route(logits.data_ptr(), ld, type_, _ptr(bias), score, groups, topk_groups, group_top,
+                               bool(renorm), scale, _ptr(rows), ids.data_ptr(), weights.data_ptr(), T, E, k, stream))
+    return ids, weights
+
+
+def moe_route_backward(dweights, logits, ids, score=BS_SCORE_SOFTMAX, renorm=True, scale=1.0, dlogits=None):
+    """Gradient of moe_route's weights: dlogits [T, E] of the logits' type, every
+    value written.  ids from moe_route; score, renorm, scale as there."""
+    fn = "moe_route_backward"
+    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2, fn, "logits must be a 2-D tensor [T, E]")
+    T, E = logits.shape
+    type_, ld = _moe_logits(fn, "logits", logits, (T, E))
+    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, fn, "ids must be a 2-D tensor [T, k]")
+    k = ids.shape[1]
+    _arg(fn, "ids", ids, (T, k), _I32, contiguous=True)
+    _arg(fn, "dweights", dweights, (T, k), _F32, contiguous=True)
+    if dlogits is None:
+        dlogits = _rows(T, E, logits.dtype, logits.device)
+    _need(dlogits.dtype == logits.dtype, fn, f"dlogits has dtype {dlogits.dtype}, the logits {logits.dtype}")
+    _, ldd = _moe_logits(fn, "dlogits", dlogits, (T, E))
+    stream = _on_current(fn, dweights, logits, ids, dlogits)
+    _check(fn, lib().moe_route_backward(dweights.data_ptr(), logits.data_ptr(), ld, type_, ids.data_ptr(), score,
+                                        bool(renorm), scale, dlogits.data_ptr(), ldd, T, E, k, stream))
+    return dlogits
+
+
 def moe_sort(ids, E, rows=None, pos=None, offsets=None, ws=None):
     """Sort the (token, expert) pairs by expert.  ids: int32 [T, k], ids outside
     [0, E) are dropped.  -> (rows int32 [T*k]: token of each slot, -1 past the

@@ -25,6 +25,12 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
                            const int* rows, const uint8_t* w, size_t w_scales, size_t w_stride, uint16_t* c,
                            int64_t ldc, int S, int Ma, int E, int N, int K, hipStream_t st);
 size_t bs_w4a4_workspace(int M, int N, int K);
+int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t* w, const float* wsc, uint16_t* c,
+                   int64_t ldc, int M, int N, int K, void* ws, hipStream_t st);
+int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const int* offsets, const int* rows,
+                           const uint8_t* w, size_t w_stride, const float* wsc, uint16_t* c, int64_t ldc, int S,
+                           int Ma, int E, int N, int K, hipStream_t st);
+size_t bs_w8a8_workspace(int M, int N, int K);
 size_t bs_moe_sort_workspace(int T, int k, int E);
 
 namespace {
@@ -80,6 +86,12 @@ bool mx_desc_ok(const bs_wdesc* d, int N, int K) {
          d->codes_bytes == codes && d->scales_offset == off && d->scales_bytes == scales &&
          d->total_bytes == off + scales;
 }
+bool i8_desc_ok(const bs_wdesc* d, int N, int K) {
+  const uint64_t bytes = static_cast<uint64_t>((N + 15) / 16) * ((K + 63) / 64) * 1024;
+  return d->magic == BS_WDESC_MAGIC && d->layout == BS_LAYOUT_INT8 && d->N == N && d->K == K &&
+         d->codes_bytes == bytes && d->scales_offset == 0 && d->scales_bytes == 0 && d->total_bytes == bytes;
+}
+bool i8_shape_ok(int N, int K) { return N >= 1 && N <= (1 << 24) && K >= 16 && K % 16 == 0 && K < (1 << 17); }
 }  // namespace
 
 BS_API size_t bs_workspace_bytes(int op, int M, int N, int K) {
@@ -98,6 +110,10 @@ BS_API size_t bs_workspace_bytes(int op, int M, int N, int K) {
   if (op == BS_OP_W4A4_MXFP4) {
     if (M < 1 || M > (1 << 22) || N < 16 || N % 16 || K < 128 || K % 128) return 0;
     return bs_w4a4_workspace(M, N, K);
+  }
+  if (op == BS_OP_W8A8_INT8) {
+    if (M < 1 || M > (1 << 22) || !i8_shape_ok(N, K)) return 0;
+    return bs_w8a8_workspace(M, N, K);
   }
   if (op == BS_OP_MOE_SORT) return bs_moe_sort_workspace(M, N, K);
   return 0;
@@ -233,6 +249,45 @@ BS_API int bsgemm_w4a4_mxfp4_grouped(const void* a, int64_t lda, const void* a_s
   return bs_launch_w4a4_grouped(static_cast<const uint8_t*>(a), lda, static_cast<const uint8_t*>(a_scale), ld_scale,
                                 offsets, rows, static_cast<const uint8_t*>(w_pre), wd->scales_offset, w_stride,
                                 static_cast<uint16_t*>(c), ldc, S, Ma, E, N, K, static_cast<hipStream_t>(stream));
+}
+
+BS_API int bsgemm_w8a8_int8(const void* a, int64_t lda, const float* a_scale, const bs_wdesc* wd, const void* w_pre,
+                            const float* w_scale, void* c, int64_t ldc, int M, int N, int K, void* ws,
+                            size_t ws_bytes, bs_stream_t stream) {
+  if (M == 0) return BS_OK;  // an empty batch: nothing is read or launched
+  BS_CHECK(a && a_scale && wd && w_pre && w_scale && c, BS_ERR_NULL);
+  BS_CHECK(M >= 1 && M <= (1 << 22) && i8_shape_ok(N, K), BS_ERR_SHAPE);
+  BS_CHECK(i8_desc_ok(wd, N, K), BS_ERR_LAYOUT);
+  BS_CHECK(lda >= K && lda % 16 == 0 && ldc >= N, BS_ERR_ALIGN);
+  BS_CHECK(bs_aligned(a, 16) && bs_aligned(w_pre, 256) && bs_aligned(c, 2) && bs_aligned(a_scale, 4) &&
+               bs_aligned(w_scale, 4),
+           BS_ERR_ALIGN);
+  BS_CHECK(lda < (1 << 24), BS_ERR_SHAPE);  // the 256 rows of a tile are addressed with 32-bit offsets
+  const int wst = check_workspace(bs_w8a8_workspace(M, N, K), ws, ws_bytes);
+  if (wst != BS_OK) return wst;
+  return bs_launch_w8a8(static_cast<const uint8_t*>(a), lda, a_scale, static_cast<const uint8_t*>(w_pre), w_scale,
+                        static_cast<uint16_t*>(c), ldc, M, N, K, ws, static_cast<hipStream_t>(stream));
+}
+
+BS_API int bsgemm_w8a8_int8_grouped(const void* a, int64_t lda, const float* a_scale, int Ma, const int32_t* offsets,
+                                    const int32_t* rows, const bs_wdesc* wd, const void* w_pre, size_t w_stride,
+                                    const float* w_scale, void* c, int64_t ldc, int S, int E, int N, int K,
+                                    bs_stream_t stream) {
+  if (S == 0) return BS_OK;  // no slots: nothing is read or launched
+  BS_CHECK(a && a_scale && offsets && wd && w_pre && w_scale && c, BS_ERR_NULL);
+  BS_CHECK(S >= 1 && S <= (1 << 24) && Ma >= 1 && Ma <= (1 << 24) && E >= 1 && E <= kMaxExperts && i8_shape_ok(N, K),
+           BS_ERR_SHAPE);
+  BS_CHECK(i8_desc_ok(wd, N, K), BS_ERR_LAYOUT);
+  BS_CHECK(w_stride >= wd->total_bytes && w_stride % 256 == 0, BS_ERR_LAYOUT);
+  BS_CHECK(lda >= K && lda % 16 == 0 && ldc >= N, BS_ERR_ALIGN);
+  BS_CHECK(bs_aligned(a, 16) && bs_aligned(w_pre, 256) && bs_aligned(c, 2) && bs_aligned(a_scale, 4) &&
+               bs_aligned(w_scale, 4) && bs_aligned(offsets, 4) && bs_aligned(rows, 4),
+           BS_ERR_ALIGN);
+  // rows are gathered with unsigned 32-bit offsets
+  BS_CHECK(lda < (1 << 24) && static_cast<uint64_t>(Ma) * lda < (1ull << 32), BS_ERR_SHAPE);
+  return bs_launch_w8a8_grouped(static_cast<const uint8_t*>(a), lda, a_scale, offsets, rows,
+                                static_cast<const uint8_t*>(w_pre), w_stride, w_scale, static_cast<uint16_t*>(c), ldc,
+                                S, Ma, E, N, K, static_cast<hipStream_t>(stream));
 }
 
 BS_API int gemm_bf16_skinny(const void* x, const void* w, void* c, int M, int N, int K, void* ws, size_t ws_bytes,

@@ -12,6 +12,8 @@
 //   MXFP4      1 KiB per (nt, ks): 16 packed bytes per lane (its 32 values);
 //              then e8m0 scales, one dword per lane per (nt, group of four
 //              steps), byte ks%4, pad 0x7F.
+//   int8       1 KiB per (nt, 64-wide step): 16 bytes per lane, K = 64*ks +
+//              16*(l/16) .. +15; rows and K past the end are zeros.
 // Every kernel moves 16-byte chunks except the scale gather (4 bytes).
 #include "common.h"
 
@@ -101,9 +103,30 @@ __global__ __launch_bounds__(kThreads) void k_mx_scales_inv(const uint32_t* __re
   }
 }
 
+// int8: chunk i = (nt*KS + ks)*64 + lane -> row n, chunk 4*ks + lane/16 of KC a row
+__global__ __launch_bounds__(kThreads) void k_i8_pre(const uint4* __restrict__ src, uint4* __restrict__ dst,
+                                                     size_t nchunks, int KS, int N, int KC, bool inverse) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= nchunks) return;
+  const int lane = static_cast<int>(i & 63);
+  const size_t t = i >> 6;
+  const size_t n = t / KS * 16 + (lane & 15);
+  const int kc = static_cast<int>(t % KS) * 4 + (lane >> 4);
+  const bool in = n < static_cast<size_t>(N) && kc < KC;
+  if (inverse) {
+    if (in) dst[n * KC + kc] = src[i];
+  } else {
+    dst[i] = in ? src[n * KC + kc] : make_uint4(0, 0, 0, 0);
+  }
+}
+
 inline unsigned blocks_for(size_t n) { return static_cast<unsigned>((n + kThreads - 1) / kThreads); }
 
 bool shape_ok(int N, int K) { return N >= 16 && N % 16 == 0 && K >= 128 && K % 128 == 0; }
+
+// (products of two 8-bit codes, summed in int32 without overflow: K < 2^17)
+bool i8_shape_ok(int N, int K) { return N >= 1 && N <= (1 << 24) && K >= 16 && K % 16 == 0 && K < (1 << 17); }
+uint64_t i8_bytes(int N, int K) { return static_cast<uint64_t>((N + 15) / 16) * ((K + 63) / 64) * 1024; }
 
 uint64_t mx_codes_bytes(int N, int K) { return static_cast<uint64_t>(N) * K / 2; }
 uint64_t mx_scale_bytes(int N, int K) { return static_cast<uint64_t>(N / 16) * ((K / 128 + 3) / 4) * 256; }
@@ -189,6 +212,35 @@ BS_API int bs_unprelayout_mxfp4(const bs_wdesc* d, const void* pre, void* wp, vo
   k_mx_scales_inv<<<blocks_for(ndw), kThreads, 0, st>>>(
       reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pre) + d->scales_offset),
       static_cast<uint8_t*>(e8), ndw, K / 128, (K / 128 + 3) / 4, K / 32);
+  return bs_launch_status();
+}
+
+BS_API size_t bs_prelayout_int8_bytes(int N, int K) {
+  return i8_shape_ok(N, K) ? static_cast<size_t>(i8_bytes(N, K)) : 0;
+}
+
+BS_API int bs_prelayout_int8(const void* w, void* out, size_t out_bytes, int N, int K, bs_wdesc* desc,
+                             bs_stream_t stream) {
+  BS_CHECK(w && out && desc, BS_ERR_NULL);
+  BS_CHECK(i8_shape_ok(N, K), BS_ERR_SHAPE);
+  BS_CHECK(bs_aligned(w, 16) && bs_aligned(out, 256), BS_ERR_ALIGN);
+  const uint64_t bytes = i8_bytes(N, K);
+  BS_CHECK(out_bytes >= bytes, BS_ERR_ARG);
+  k_i8_pre<<<blocks_for(bytes / 16), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+      static_cast<const uint4*>(w), static_cast<uint4*>(out), bytes / 16, (K + 63) / 64, N, K / 16, false);
+  const int st = bs_launch_status();
+  if (st != BS_OK) return st;
+  *desc = bs_wdesc{BS_WDESC_MAGIC, BS_LAYOUT_INT8, N, K, bytes, 0, 0, bytes};
+  return BS_OK;
+}
+
+BS_API int bs_unprelayout_int8(const bs_wdesc* d, const void* pre, void* w, bs_stream_t stream) {
+  BS_CHECK(d && pre && w, BS_ERR_NULL);
+  BS_CHECK(d->magic == BS_WDESC_MAGIC && d->layout == BS_LAYOUT_INT8 && i8_shape_ok(d->N, d->K), BS_ERR_LAYOUT);
+  BS_CHECK(bs_aligned(w, 16) && bs_aligned(pre, 256), BS_ERR_ALIGN);
+  const size_t nchunks = i8_bytes(d->N, d->K) / 16;
+  k_i8_pre<<<blocks_for(nchunks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
+      static_cast<const uint4*>(pre), static_cast<uint4*>(w), nchunks, (d->K + 63) / 64, d->N, d->K / 16, true);
   return bs_launch_status();
 }
 

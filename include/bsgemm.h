@@ -87,10 +87,14 @@ BS_API int bs_version(void);
  *               (nt, 4 consecutive ks) 256 B: lane l's dword holds the scales
  *               of its row and K-block l/16 for those four steps (byte = ks%4;
  *               unused bytes of a final partial dword are 0x7F).
+ *   int8:       K steps of 64: per (nt, ks) 1 KiB, lane l's 16 bytes
+ *               W[n][64ks + 16(l/16) .. +16] at offset 16*l; rows past N and
+ *               bytes past K are zeros.
  */
 enum {
   BS_LAYOUT_FP8_BLOCK = 0x38423631, /* e4m3 codes, 16x128 fragment order   */
-  BS_LAYOUT_MXFP4 = 0x34584D31      /* e2m1 codes + e8m0, fragment order   */
+  BS_LAYOUT_MXFP4 = 0x34584D31,     /* e2m1 codes + e8m0, fragment order   */
+  BS_LAYOUT_INT8 = 0x38544E49       /* int8 codes, 16x64 fragment order    */
 };
 #define BS_WDESC_MAGIC 0x42534744u
 
@@ -127,6 +131,16 @@ BS_API int bs_prelayout_mxfp4(const void* w_packed, const void* w_e8m0, void* ou
 BS_API int bs_unprelayout_mxfp4(const bs_wdesc* desc, const void* pre, void* w_packed, void* w_e8m0,
                                 bs_stream_t stream);
 
+/* Bytes needed for a pre-laid-out int8 weight, 0 on bad shape. */
+BS_API size_t bs_prelayout_int8_bytes(int N, int K);
+/* w: [N, K] int8, row-major.  1 <= N <= 2^24, 16 <= K < 2^17, K % 16 == 0.
+ * w 16-byte, out 256-byte aligned.  The scales (fp32, one per row of w) are not
+ * moved: they are passed to the GEMM as they are. */
+BS_API int bs_prelayout_int8(const void* w, void* out, size_t out_bytes, int N, int K, bs_wdesc* desc,
+                             bs_stream_t stream);
+/* Exact inverse: back to [N, K] int8. */
+BS_API int bs_unprelayout_int8(const bs_wdesc* desc, const void* pre, void* w, bs_stream_t stream);
+
 /* ---------------------------------------------------------- workspaces
  * Some shapes split K across workgroups and reduce through a caller-provided
  * workspace (int32 counters + fp32 partial slab, as the pages' decode split-K
@@ -153,7 +167,8 @@ enum {
   BS_OP_W4A8_MXFP4 = 2,
   BS_OP_BF16_SKINNY = 3,
   BS_OP_W4A4_MXFP4 = 4,
-  BS_OP_MOE_SORT = 5 /* M, N, K = tokens, experts per token, experts */
+  BS_OP_MOE_SORT = 5, /* M, N, K = tokens, experts per token, experts */
+  BS_OP_W8A8_INT8 = 6
 };
 BS_API size_t bs_workspace_bytes(int op, int M, int N, int K);
 
@@ -296,6 +311,35 @@ BS_API int bsgemm_w4a4_mxfp4_grouped(const void* a, int64_t lda, const void* a_s
                                      const void* w_pre, size_t w_stride, void* c, int64_t ldc, int S, int E, int N,
                                      int K, bs_stream_t stream);
 
+/* int8 GEMM: int8 codes on both sides, one scale per activation row and one per
+ * weight row (output channel):
+ *   C[m,n] = bf16( fp32( sum_k a[m,k] * w[n,k] ) * a_scale[m] * w_scale[n] )
+ * the sum exact (int32, K < 2^17), then rounded to fp32; the two products in
+ * fp32, in this order.
+ * a: int8 [M, K] (lda bytes, a multiple of 16): what add_rms_quant_int8,
+ * silu_mul_quant_int8 and quant_int8_per_token write; a_scale: fp32 [M]; w_pre:
+ * pre-laid-out by bs_prelayout_int8 (desc wd); w_scale: fp32 [N]; c: bf16
+ * [M, N] (ldc elements; rows that are not 16-byte aligned are stored value by
+ * value).  Needs 1 <= M <= 2^22, 1 <= N <= 2^24, 16 <= K < 2^17, K % 16 == 0,
+ * lda < 2^24; a 16-byte, w_pre 256-byte, the scales 4-byte aligned.
+ * ws: bs_workspace_bytes(BS_OP_W8A8_INT8, M, N, K) bytes (256-byte aligned,
+ * zeroed once); when that is 0, ws may be NULL. */
+BS_API int bsgemm_w8a8_int8(const void* a, int64_t lda, const float* a_scale, const bs_wdesc* wd, const void* w_pre,
+                            const float* w_scale, void* c, int64_t ldc, int M, int N, int K, void* ws,
+                            size_t ws_bytes, bs_stream_t stream);
+
+/* The same product for the experts of a mixture, over slots sorted by expert
+ * (see bsgemm_w4a4_mxfp4_grouped for offsets, rows, S, E and w_stride):
+ *   C[s,:] = the product of row rows[s] and expert e   for offsets[e] <= s < offsets[e+1]
+ * a_scale: fp32 [Ma]; w_scale: fp32 [E, N] dense.  Rows of slots past offsets[E]
+ * are left as they are; offsets and rows are read on the device only and
+ * clamped.  Needs Ma <= 2^24, Ma * lda < 2^32 and the limits above.  No
+ * workspace. */
+BS_API int bsgemm_w8a8_int8_grouped(const void* a, int64_t lda, const float* a_scale, int Ma, const int32_t* offsets,
+                                    const int32_t* rows, const bs_wdesc* wd, const void* w_pre, size_t w_stride,
+                                    const float* w_scale, void* c, int64_t ldc, int S, int E, int N, int K,
+                                    bs_stream_t stream);
+
 /* ----------------------------------------------------------- producers */
 
 /* Fused residual add + Gemma RMSNorm + per-token e4m3 quant (radiance_arnq.py
@@ -393,10 +437,84 @@ BS_API int silu_mul_quant_mxfp4(const void* gu, void* q, void* scale, const int3
  * q 4-byte, out 16-byte aligned. */
 BS_API int dequant_mxfp4(const void* q, const void* scale, void* out, int M, int K, bs_stream_t stream);
 
+/* int8 quant, one scale per row: for a row h of fp32 values
+ *   scale = max(fp32(max |h| / 127), 2^-126)
+ *   q     = h / scale, the exact quotient rounded to nearest even (-127 .. 127)
+ * exact (codes and scales are the definition's, bit for bit).  A row with an
+ * infinity or a NaN gets a NaN scale and zero codes, so every product that reads
+ * it is NaN.
+ * quant_int8_per_token: h = x.  x: bf16 [M, K] (ldx elements, a multiple of 8);
+ * q: int8 [M, K] dense; scale: fp32 [M].  On a weight [N, K] this gives the codes
+ * for bs_prelayout_int8 and w_scale.  K % 8 == 0, 8 <= K <= 32768; x 16-byte, q
+ * 8-byte aligned. */
+BS_API int quant_int8_per_token(const void* x, int64_t ldx, void* q, float* scale, int M, int K, bs_stream_t stream);
+
+/* Residual add + RMSNorm + the same quant (as add_rms_quant_fp8):
+ *   r = bf16(y + residual)                    -> residual_out (bf16 [M, K])
+ *   h = fp32( r / sqrt(mean_k r^2 + eps) * (offset + gamma) ), the real value rounded once
+ * offset is 1 for a norm whose weight is stored as its distance from one, 0 for a
+ * plain one.  residual may be NULL: then r = y and residual_out may be NULL too
+ * (it is not written).  residual_out may equal residual; no other overlap.
+ * y, residual, residual_out: bf16 [M, K] dense; gamma: bf16 [K]; offset finite.
+ * K % 8 == 0, 8 <= K <= 32768; pointers 16-byte, q 8-byte aligned. */
+BS_API int add_rms_quant_int8(const void* y, const void* residual, const void* gamma, float eps, float offset, void* q,
+                              float* scale, void* residual_out, int M, int K, bs_stream_t stream);
+
+/* SiLU(gate) * up + the same quant:  h = fp32(g / (1 + exp(-g)) * u), the real
+ * value rounded once, g = gu[m, k], u = gu[m, N + k].  gu: bf16 [M, 2N] dense
+ * (gate half first); q: int8 [M, N]; scale: fp32 [M].  rows: NULL, or a device
+ * int32: only the first min(*rows, M) rows are computed, the rest left as they
+ * are.  N % 8 == 0, 8 <= N <= 32768; gu 16-byte, q 8-byte, rows 4-byte aligned. */
+BS_API int silu_mul_quant_int8(const void* gu, void* q, float* scale, const int32_t* rows, int M, int N,
+                               bs_stream_t stream);
+
+/* The values that int8 codes stand for: out[m, k] = bf16(q[m, k] * scale[m]),
+ * rounded once.  q: int8 [M, K]; out: bf16 [M, K]; dense.  K % 8 == 0,
+ * M * K / 8 < 2^31; q 8-byte, out 16-byte aligned. */
+BS_API int dequant_int8(const void* q, const float* scale, void* out, int M, int K, bs_stream_t stream);
+
 /* ------------------------------------------------- mixture of experts
  * Pair p = t * k + j is the j-th choice of token t.  Every sum over j runs in
  * its order and every result is deterministic.  Outputs overlap neither inputs
  * nor each other. */
+
+/* The choice of k experts for each token from its logits, and their weights.
+ *   s[e] = softmax over e of logits[t, e]            (score BS_SCORE_SOFTMAX)
+ *          or 1 / (1 + exp(-logits[t, e]))           (BS_SCORE_SIGMOID)
+ *   v[e] = s[e] + bias[e]
+ * An expert with logit -inf, or v = -inf, is off.  With groups > 1 the experts
+ * are cut into that many runs of E / groups; a group counts as the sum of its
+ * group_top (1 or 2) largest v, and the experts outside the topk_groups groups
+ * that count most are off too.
+ *   ids[t, j]      the expert with the j-th largest v; -1 when no more are on
+ *   weights[t, j]  scale * s[ids], divided by the sum of the chosen s with renorm
+ *                  != 0 (0 where that sum is 0); 0 for -1
+ * Equal v, and groups that count the same, in the order of their index.  Scores
+ * and their sums are compared in 64 bits (without a bias, experts by their
+ * logits), so ids are the definition's.  A NaN v, or a group's NaN, comes after
+ * every number; weights of a softmax over a NaN or +inf are NaN.
+ * logits: fp32 or bf16 (type BS_TYPE_F32, BS_TYPE_BF16) [T, E], ld elements, ld
+ * >= E; bias: fp32 [E] or NULL (it is not part of the weights).  rows: NULL, or
+ * a device int32: tokens from *rows on (padding) get ids -1 and weights 0, their
+ * logits are not used.  ids: int32, weights: fp32 [T, k], dense.  1 <= E <= 1024,
+ * 1 <= k <= min(E, 64), 1 <= topk_groups <= groups <= 64, groups divides E,
+ * topk_groups * (E / groups) >= k, E / groups >= group_top, T <= 2^24; pointers
+ * aligned to their type. */
+enum { BS_TYPE_F32 = 0, BS_TYPE_BF16 = 1 };
+enum { BS_SCORE_SOFTMAX = 0, BS_SCORE_SIGMOID = 1 };
+BS_API int moe_route(const void* logits, int64_t ld, int type, const float* bias, int score, int groups,
+                     int topk_groups, int group_top, int renorm, float scale, const int32_t* rows, int32_t* ids,
+                     float* weights, int T, int E, int k, bs_stream_t stream);
+
+/* The gradient of moe_route's weights for dweights = d/d weights (fp32 [T, k]):
+ *   dlogits[t, e] = sum_j dweights[t, j] * d weights[t, j] / d logits[t, e]
+ * of the logits' type, [T, E] (ldd elements), every value written (zero where
+ * nothing depends on it).  ids as moe_route wrote them; an id outside [0, E) has
+ * no part, one that is there twice counts twice.  The choice, and so the bias,
+ * has no gradient.  Other arguments and limits as moe_route. */
+BS_API int moe_route_backward(const float* dweights, const void* logits, int64_t ld, int type, const int32_t* ids,
+                              int score, int renorm, float scale, void* dlogits, int64_t ldd, int T, int E, int k,
+                              bs_stream_t stream);
 
 /* Sort the pairs by expert (stable: equal ids keep the order of p).
  * ids: int32 [T, k]; a pair whose id is outside [0, E) is dropped (a padded

@@ -1,0 +1,196 @@
+"""int8 GEMMs against the oracle, bit for bit: the sums are whole numbers, exact in
+int32 here and in fp64 there, and what follows is three fp32 roundings in a fixed
+order and one to bf16."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_04_amd as bs
+from oracle import codecs, int8
+from tests.gpu_util import host_bits16
+
+pytestmark = pytest.mark.gpu
+
+
+def _codes(seed, shape, full=True):
+    g = np.random.default_rng(seed)
+    if full:
+        return g.integers(-128, 128, shape).astype(np.int8)
+    return np.clip(np.rint(g.standard_normal(shape) * 35), -127, 127).astype(np.int8)
+
+
+def _scales(seed, n):
+    return np.exp(np.random.default_rng(seed).uniform(-9, -3, n)).astype(np.float32)
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _check(out, a, sa, w, sw, what=""):
+    torch.cuda.synchronize()
+    got, want = host_bits16(out), int8.gemm(a, sa, w, sw)
+    bad = np.argwhere(got != want)
+    assert not len(bad), (f"{what}: {len(bad)} of {got.size} differ, first {bad[:3].tolist()}: "
+                          f"{codecs.decode_bf16(got[tuple(bad[0])])}, want {codecs.decode_bf16(want[tuple(bad[0])])}")
+
+
+def _run(M, N, K, out=None, seed=0):
+    a, w = _codes(M + seed, (M, K)), _codes(N + K + seed, (N, K))
+    sa, sw = _scales(M, M), _scales(N, N)
+    pre, desc = bs.prelayout_int8(_dev(w))
+    c = bs.bsgemm_w8a8_int8(_dev(a), _dev(sa), desc, pre, _dev(sw), out=out,
+                            ws=bs.alloc_workspace(bs.BS_OP_W8A8_INT8, M, N, K))
+    _check(c, a, sa, w, sw, f"M={M} N={N} K={K}")
+
+
+@pytest.mark.parametrize("N,K", [(16, 64), (1, 16), (21, 80), (256, 512), (1000, 1040)])
+def test_prelayout_round_trip(N, K):
+    w = _codes(1, (N, K))
+    pre, desc = bs.prelayout_int8(_dev(w))
+    assert np.array_equal(pre.cpu().numpy(), int8.prelayout(w))
+    assert np.array_equal(bs.unprelayout_int8(desc, pre).cpu().numpy(), w)
+
+
+SHAPES = [
+    # one row, the smallest sizes, sizes that are no multiple of anything
+    (1, 1, 16), (1, 16, 64), (2, 17, 80), (3, 33, 16), (1, 5120, 5120), (5, 129, 1040),
+    # few rows
+    (7, 256, 512), (8, 1024, 2048), (16, 640, 5120), (17, 640, 5120), (31, 300, 464), (32, 512, 1024),
+    (33, 2048, 768), (48, 512, 12288), (64, 1000, 1936), (64, 5120, 640), (8, 4096, 17408), (1, 100, 131056),
+    (16, 17408, 1024), (9, 34000, 256), (8, 1024, 64), (12, 272, 192), (3, 2000, 320),
+    # many rows
+    (65, 512, 5120), (100, 129, 528), (127, 640, 64), (128, 128, 128), (129, 257, 192), (255, 1000, 320),
+    (256, 2048, 1024), (301, 1280, 2560), (512, 768, 4096), (1000, 1024, 64), (1025, 2050, 528), (2000, 33, 16),
+    (1, 70000, 64), (4100, 16, 256), (3000, 1500, 272), (2048, 2048, 1024), (40, 40, 131056),
+]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(M, N, K):
+    _run(M, N, K)
+
+
+def test_largest_sums():
+    """K = 131056 of the largest products: the sum is next to 2^31."""
+    for M in (1, 20, 70):
+        a, w = np.full((M, 131056), -128, np.int8), np.full((3, 131056), -128, np.int8)
+        w[1] = 127
+        w[2] = 0
+        sa, sw = np.full(M, 2.0 ** -20, np.float32), np.full(3, .5, np.float32)
+        pre, desc = bs.prelayout_int8(_dev(w))
+        c = bs.bsgemm_w8a8_int8(_dev(a), _dev(sa), desc, pre, _dev(sw),
+                                ws=bs.alloc_workspace(bs.BS_OP_W8A8_INT8, M, 3, 131056))
+        _check(c, a, sa, w, sw)
+
+
+def test_scales_at_the_ends():
+    """NaN, infinite, subnormal and huge scales go through the same fp32 products."""
+    M, N, K = 70, 48, 128
+    for m in (5, M):
+        a, w = _codes(1, (m, K)), _codes(2, (N, K))
+        sa, sw = _scales(3, m), _scales(4, N)
+        sa[:5] = [np.nan, np.inf, 1e-40, 3e38, 0.0]
+        sw[:5] = [1e-42, 3e38, np.nan, 1.0, -2.0]
+        pre, desc = bs.prelayout_int8(_dev(w))
+        c = bs.bsgemm_w8a8_int8(_dev(a), _dev(sa), desc, pre, _dev(sw))
+        got, want = codecs.decode_bf16(host_bits16(c)), codecs.decode_bf16(int8.gemm(a, sa, w, sw))
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("M", [3, 20, 90, 400])
+@pytest.mark.parametrize("N,pad", [(256, 8), (256, 3), (251, 0), (251, 5), (120, 8), (13, 0)])
+def test_strides(M, N, pad):
+    """Padded rows of both sides, outputs at any alignment; what lies between the
+    rows of the output stays as it was, behind the activations anything may stand."""
+    K, lda = 272, 272 + 48
+    a, w = _codes(1, (M, lda)), _codes(2, (N, K))
+    sa, sw = _scales(3, M), _scales(4, N)
+    pre, desc = bs.prelayout_int8(_dev(w))
+    for shift in (0, 1, 4):
+        buf = torch.full((M * (N + pad) + shift,), 7.0, dtype=torch.bfloat16, device="cuda")
+        c = buf[shift:].view(M, N + pad)[:, :N]
+        bs.bsgemm_w8a8_int8(_dev(a)[:, :K], _dev(sa), desc, pre, _dev(sw), out=c,
+                            ws=bs.alloc_workspace(bs.BS_OP_W8A8_INT8, M, N, K))
+        _check(c, a[:, :K], sa, w, sw, f"shift {shift}")
+        rest = buf[shift:].view(M, N + pad)[:, N:]
+        assert bool((rest == 7.0).all()) and bool((buf[:shift] == 7.0).all())
+
+
+def test_activations_end_with_their_buffer():
+    """The last row ends where its allocation does (K is no multiple of 64)."""
+    for M in (1, 9, 40, 100):
+        K = 2048 + 16
+        n = M * K
+        buf = torch.empty(n, dtype=torch.int8, device="cuda")
+        a, w = _codes(M, (M, K)), _codes(2, (80, K))
+        buf.copy_(_dev(a).reshape(-1))
+        pre, desc = bs.prelayout_int8(_dev(w))
+        sa, sw = _scales(3, M), _scales(4, 80)
+        c = bs.bsgemm_w8a8_int8(buf.view(M, K), _dev(sa), desc, pre, _dev(sw),
+                                ws=bs.alloc_workspace(bs.BS_OP_W8A8_INT8, M, 80, K))
+        _check(c, a, sa, w, sw)
+
+
+def test_empty_batch():
+    pre, desc = bs.prelayout_int8(_dev(_codes(1, (32, 64))))
+    e = torch.empty((0, 64), dtype=torch.int8, device="cuda")
+    z = torch.empty((0,), device="cuda")
+    assert bs.bsgemm_w8a8_int8(e, z, desc, pre, torch.ones(32, device="cuda")).shape == (0, 32)
+
+
+# ------------------------------------------------------------------ grouped
+def _offsets(kind, E, S, seed):
+    g = np.random.default_rng(seed)
+    if kind == "even":
+        return np.linspace(0, S, E + 1).astype(np.int32)
+    if kind == "one":                       # all slots with one expert
+        o = np.zeros(E + 1, np.int32)
+        o[E // 2 + 1:] = S
+        return o
+    if kind == "short":                     # slots past the last expert
+        return np.sort(np.concatenate([[0], g.integers(0, S * 3 // 4 + 1, E)])).astype(np.int32)
+    return np.sort(np.concatenate([[0], g.integers(0, S + 1, E - 1), [S]])).astype(np.int32)
+
+
+def _grouped(E, S, N, K, kind, rows=True, seed=0, Ma=None):
+    g = np.random.default_rng(seed)
+    Ma = S if not rows else (Ma or max(1, S // 3))
+    a, w = _codes(seed, (Ma, K)), _codes(seed + 1, (E, N, K))
+    sa, sw = _scales(seed, Ma), _scales(seed + 1, E * N).reshape(E, N)
+    o = _offsets(kind, E, S, seed)
+    src = g.integers(0, Ma, S).astype(np.int32) if rows else np.arange(S)
+    pre, desc = bs.prelayout_int8_experts(_dev(w))
+    out = torch.full((S, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    bs.bsgemm_w8a8_int8_grouped(_dev(a), _dev(sa), _dev(o), desc, pre, _dev(sw), rows=_dev(src) if rows else None,
+                                out=out)
+    for e in range(E):
+        r = src[o[e]:o[e + 1]]
+        if len(r):
+            _check(out[o[e]:o[e + 1]], a[r], sa[r], w[e], sw[e], f"expert {e}")
+    assert bool((out[o[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("E,S,N,K,kind,rows", [
+    (1, 1, 16, 64, "even", True), (4, 7, 48, 192, "any", True), (8, 40, 129, 80, "any", True),
+    (16, 100, 256, 512, "short", True), (5, 333, 200, 272, "any", False), (64, 64, 128, 256, "one", True),
+    (256, 128, 64, 128, "any", True), (3, 2000, 130, 64, "any", True), (2, 1000, 512, 1024, "even", False),
+    (4, 900, 384, 2048, "short", True), (300, 4000, 40, 64, "any", True), (1024, 1024, 16, 16, "any", True),
+    (7, 50, 1000, 1040, "any", True), (16, 300, 264, 2112, "any", False), (8, 8, 2048, 2048, "any", True),
+    (10, 12, 512, 5120, "any", True), (6, 200, 72, 8192, "any", True), (2, 5, 1024, 131056, "even", True)])
+def test_grouped(E, S, N, K, kind, rows):
+    _grouped(E, S, N, K, kind, rows, seed=E + S)
+
+
+def test_grouped_out_of_range_indexes_stay_inside():
+    """Offsets and rows that hold anything name nothing outside the buffers."""
+    E, S, N, K = 6, 300, 64, 128
+    pre, desc = bs.prelayout_int8_experts(_dev(_codes(1, (E, N, K))))
+    a, sa = _dev(_codes(2, (50, K))), _dev(_scales(3, 50))
+    guard = torch.full((S + 64, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    for o in ([-5, 10, 2 ** 31 - 1, -2 ** 31, 40, 400, 301], [300, 200, 100, 50, 20, 10, 0], [0] * 7):
+        bs.bsgemm_w8a8_int8_grouped(a, sa, _dev(np.array(o, np.int32)), desc, pre, torch.ones((E, N), device="cuda"),
+                                    rows=_dev(np.random.default_rng(1).integers(-2 ** 31, 2 ** 31, S).astype(np.int32)),
+                                    out=guard[32:32 + S])
+        torch.cuda.synchronize()
+        assert bool((guard[:32] == 7.0).all()) and bool((guard[32 + S:] == 7.0).all())

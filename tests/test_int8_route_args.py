@@ -1,0 +1,237 @@
+"""Refusals of the int8 and routing entry points, in the C ABI and in the Python
+binding.  CPU only: every call is refused before any device memory is touched."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import block_scaled_precision_04_amd as bs
+from block_scaled_precision_04_amd import _binding
+from block_scaled_precision_04_amd._binding import WDesc, BS_WDESC_MAGIC, BS_LAYOUT_FP8_BLOCK, BS_LAYOUT_INT8
+
+FAKE = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10001)
+TWO = ctypes.c_void_p(0x10002)
+EIGHT = ctypes.c_void_p(0x10008)
+N, K = 256, 512
+
+
+@pytest.fixture(scope="module")
+def blib():
+    import os
+    if not os.path.exists(_binding.LIB_PATH):
+        from block_scaled_precision_04_amd import build
+        build.build()
+    return _binding.lib()
+
+
+def _desc(n=N, k=K):
+    b = (n + 15) // 16 * ((k + 63) // 64) * 1024
+    return WDesc(BS_WDESC_MAGIC, BS_LAYOUT_INT8, n, k, b, 0, 0, b)
+
+
+def test_prelayout(blib):
+    size = blib.bs_prelayout_int8_bytes
+    assert size(16, 64) == 1024 and size(17, 80) == 4096 and size(1, 16) == 1024
+    assert size(0, 64) == 0 and size(16, 0) == 0 and size(16, 24) == 0 and size(16, 1 << 17) == 0
+    assert size(16, (1 << 17) - 16) == 2048 * 1024 and size((1 << 24) + 1, 16) == 0
+    d = WDesc()
+
+    def call(w=FAKE, out=FAKE, nbytes=1 << 20, n=N, k=K):
+        return blib.bs_prelayout_int8(w, out, nbytes, n, k, ctypes.byref(d), None)
+    assert call(w=None) == -1 and call(out=None) == -1 and call(n=0) == -2 and call(k=40) == -2 and call(k=1 << 17) == -2
+    assert call(w=EIGHT) == -3 and call(out=ctypes.c_void_p(0x10080)) == -3 and call(nbytes=N * K - 1) == -9
+    assert blib.bs_unprelayout_int8(ctypes.byref(_desc()), None, FAKE, None) == -1
+    assert blib.bs_unprelayout_int8(ctypes.byref(_desc()), FAKE, EIGHT, None) == -3
+    bad = _desc()
+    bad.layout = BS_LAYOUT_FP8_BLOCK
+    assert blib.bs_unprelayout_int8(ctypes.byref(bad), FAKE, FAKE, None) == -4
+
+
+def test_w8a8_refusals(blib):
+    def call(M=8, n=N, k=K, a=FAKE, lda=None, s=FAKE, d=None, w=FAKE, wsc=FAKE, c=FAKE, ldc=None, ws=None, wsn=0):
+        d = _desc(n, k) if d is None else d
+        return blib.bsgemm_w8a8_int8(a, k if lda is None else lda, s, ctypes.byref(d), w, wsc, c,
+                                     n if ldc is None else ldc, M, n, k, ws, wsn, None)
+    assert call(M=0, a=None, s=None, w=None, c=None, wsc=None) == 0
+    assert call(a=None) == -1 and call(s=None) == -1 and call(w=None) == -1 and call(c=None) == -1 and call(wsc=None) == -1
+    assert call(M=-1) == -2 and call(M=(1 << 22) + 1) == -2
+    assert call(n=0, d=_desc()) == -2 and call(k=520, d=_desc()) == -2 and call(k=1 << 17, d=_desc()) == -2
+    assert call(n=240, d=_desc()) == -4 and call(k=528, d=_desc()) == -4
+    assert call(d=WDesc(BS_WDESC_MAGIC, BS_LAYOUT_FP8_BLOCK, N, K, N * K, 0, 0, N * K)) == -4
+    short = _desc()
+    short.total_bytes -= 1024
+    assert call(d=short) == -4
+    assert call(lda=K - 16) == -3 and call(lda=K + 8) == -3 and call(lda=-16) == -3 and call(ldc=N - 1) == -3
+    assert call(lda=1 << 24) == -2 and call(lda=1 << 40) == -2
+    assert call(a=EIGHT) == -3 and call(s=TWO) == -3 and call(wsc=TWO) == -3 and call(c=ODD) == -3
+    assert call(w=ctypes.c_void_p(0x10080)) == -3
+    for op in ((8, 0, 512), (8, 256, 520), (8, 256, 1 << 17), (0, 256, 512), ((1 << 22) + 1, 256, 512)):
+        assert bs.workspace_bytes(bs.BS_OP_W8A8_INT8, *op) == 0
+
+
+def test_w8a8_workspace_is_needed(blib):
+    """Every shape that asks for a workspace is refused without it, with one that is
+    too small, and with a misaligned one."""
+    seen = 0
+    for M, n, k in ((8, 256, 17408), (1, 16, 131056), (16, 5120, 5120), (64, 5120, 17408), (300, 512, 16384)):
+        need = bs.workspace_bytes(bs.BS_OP_W8A8_INT8, M, n, k)
+        if not need:
+            continue
+        seen += 1
+
+        def call(ws, wsn):
+            return blib.bsgemm_w8a8_int8(FAKE, k, FAKE, ctypes.byref(_desc(n, k)), FAKE, FAKE, FAKE, n, M, n, k, ws, wsn,
+                                         None)
+        assert call(None, 0) == -5 and call(FAKE, need - 1) == -5 and call(ctypes.c_void_p(0x10080), need) == -3
+    assert bs.workspace_bytes(bs.BS_OP_W8A8_INT8, 8192, 10240, 5120) == 0
+
+
+def test_grouped_refusals(blib):
+    def call(S=8, E=4, Ma=8, n=N, k=K, a=FAKE, lda=None, s=FAKE, off=FAKE, rows=None, d=None, w=FAKE, stride=None,
+             wsc=FAKE, c=FAKE, ldc=None):
+        d = _desc(n, k) if d is None else d
+        return blib.bsgemm_w8a8_int8_grouped(a, k if lda is None else lda, s, Ma, off, rows, ctypes.byref(d), w,
+                                             d.total_bytes if stride is None else stride, wsc, c,
+                                             n if ldc is None else ldc, S, E, n, k, None)
+    assert call(S=0, a=None, s=None, off=None, w=None, c=None, wsc=None) == 0
+    for name in ("a", "s", "off", "w", "wsc", "c"):
+        assert call(**{name: None}) == -1, name
+    assert call(S=-1) == -2 and call(S=(1 << 24) + 1) == -2 and call(E=0) == -2 and call(E=1025) == -2
+    assert call(Ma=0) == -2 and call(Ma=(1 << 24) + 1) == -2 and call(n=0, d=_desc()) == -2 and call(k=8, d=_desc()) == -2
+    assert call(n=255, d=_desc()) == -4
+    assert call(stride=N * K - 256) == -4 and call(stride=N * K + 128) == -4
+    assert call(lda=K - 16) == -3 and call(lda=K + 4) == -3 and call(ldc=N - 1) == -3
+    assert call(a=EIGHT) == -3 and call(s=TWO) == -3 and call(off=TWO) == -3 and call(rows=TWO) == -3
+    assert call(w=ctypes.c_void_p(0x10080)) == -3 and call(wsc=TWO) == -3 and call(c=ODD) == -3
+    assert call(Ma=1 << 22, lda=1 << 10) == -2 and call(lda=1 << 24) == -2
+
+
+def test_quant_refusals(blib):
+    nan = ctypes.c_float(math.nan)
+
+    def quant(x=FAKE, ldx=K, q=FAKE, s=FAKE, M=4, k=K):
+        return blib.quant_int8_per_token(x, ldx, q, s, M, k, None)
+    assert quant(M=0, x=None, q=None, s=None) == 0
+    assert quant(x=None) == -1 and quant(q=None) == -1 and quant(s=None) == -1
+    assert quant(M=-1) == -2 and quant(k=0) == -2 and quant(k=20) == -2 and quant(k=32776, ldx=32776) == -2
+    assert quant(ldx=K - 8) == -3 and quant(ldx=K + 4) == -3
+    assert quant(x=EIGHT) == -3 and quant(q=ctypes.c_void_p(0x10004)) == -3 and quant(s=TWO) == -3
+
+    def norm(y=FAKE, r=FAKE, g=FAKE, eps=1e-6, off=1.0, q=FAKE, s=FAKE, ro=FAKE, M=4, k=K):
+        return blib.add_rms_quant_int8(y, r, g, eps, off, q, s, ro, M, k, None)
+    assert norm(M=0, y=None, r=None, g=None, q=None, s=None, ro=None) == 0
+    assert norm(y=None) == -1 and norm(g=None) == -1 and norm(q=None) == -1 and norm(s=None) == -1 and norm(ro=None) == -1
+    assert norm(M=-1) == -2 and norm(k=4) == -2 and norm(k=32776) == -2
+    for name in ("y", "r", "g", "ro"):
+        assert norm(**{name: EIGHT}) == -3, name
+    assert norm(q=ctypes.c_void_p(0x10004)) == -3 and norm(s=TWO) == -3
+    assert norm(eps=-1e-6) == -9 and norm(eps=nan) == -9 and norm(off=nan) == -9 and norm(off=math.inf) == -9
+
+    def silu(gu=FAKE, q=FAKE, s=FAKE, rows=None, M=4, n=K):
+        return blib.silu_mul_quant_int8(gu, q, s, rows, M, n, None)
+    assert silu(M=0, gu=None, q=None, s=None) == 0
+    assert silu(gu=None) == -1 and silu(q=None) == -1 and silu(s=None) == -1
+    assert silu(M=-2) == -2 and silu(n=12) == -2 and silu(n=32776) == -2
+    assert silu(gu=EIGHT) == -3 and silu(q=TWO) == -3 and silu(s=TWO) == -3 and silu(rows=TWO) == -3
+
+    def deq(q=FAKE, s=FAKE, out=FAKE, M=4, k=K):
+        return blib.dequant_int8(q, s, out, M, k, None)
+    assert deq(M=0, q=None, s=None, out=None) == 0
+    assert deq(q=None) == -1 and deq(s=None) == -1 and deq(out=None) == -1
+    assert deq(M=-1) == -2 and deq(k=12) == -2 and deq(M=1 << 28, k=64) == -2
+    assert deq(q=TWO) == -3 and deq(s=TWO) == -3 and deq(out=EIGHT) == -3
+
+
+def test_route_refusals(blib):
+    def call(x=FAKE, ld=None, typ=1, bias=None, score=0, g=1, keep=1, top=1, rows=None, ids=FAKE, w=FAKE, T=8, E=64, k=4):
+        return blib.moe_route(x, E if ld is None else ld, typ, bias, score, g, keep, top, 1, 1.0, rows, ids, w, T, E, k,
+                              None)
+    assert call(T=0, x=None, ids=None, w=None) == 0
+    assert call(x=None) == -1 and call(ids=None) == -1 and call(w=None) == -1
+    assert call(T=-1) == -2 and call(T=(1 << 24) + 1) == -2 and call(E=0) == -2 and call(E=1025) == -2
+    assert call(k=0) == -2 and call(k=65, E=128) == -2 and call(k=9, E=8) == -2
+    assert call(g=0) == -2 and call(g=5) == -2 and call(g=65, E=130) == -2 and call(g=8, keep=9) == -2
+    assert call(g=8, keep=0) == -2 and call(g=8, keep=2, top=3) == -2 and call(g=8, keep=2, top=0) == -2
+    assert call(g=64, keep=8, top=2) == -2          # groups of one expert
+    assert call(g=16, keep=1, k=5) == -2            # the groups that stay hold four
+    assert call(typ=2) == -9 and call(typ=-1) == -9 and call(score=2) == -9
+    assert call(ld=63) == -3 and call(x=ODD) == -3 and call(x=TWO, typ=0) == -3 and call(bias=TWO) == -3
+    assert call(rows=TWO) == -3 and call(ids=TWO) == -3 and call(w=TWO) == -3
+
+    def back(dw=FAKE, x=FAKE, ld=None, typ=1, ids=FAKE, score=0, d=FAKE, ldd=None, T=8, E=64, k=4):
+        return blib.moe_route_backward(dw, x, E if ld is None else ld, typ, ids, score, 1, 1.0, d,
+                                       E if ldd is None else ldd, T, E, k, None)
+    assert back(T=0, dw=None, x=None, ids=None, d=None) == 0
+    assert back(dw=None) == -1 and back(x=None) == -1 and back(ids=None) == -1 and back(d=None) == -1
+    assert back(T=-1) == -2 and back(E=1025) == -2 and back(k=0) == -2 and back(k=65, E=128) == -2 and back(k=9, E=8) == -2
+    assert back(typ=3) == -9 and back(score=-1) == -9
+    assert back(ld=63) == -3 and back(ldd=63) == -3 and back(x=ODD) == -3 and back(d=ODD) == -3
+    assert back(d=TWO, typ=0) == -3 and back(dw=TWO) == -3 and back(ids=TWO) == -3
+
+
+# ------------------------------------------------------------------ the binding
+def _i8(*shape):
+    return torch.zeros(shape, dtype=torch.int8)
+
+
+def _f32(*shape):
+    return torch.zeros(shape)
+
+
+def _bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def _i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+REFUSED = [
+    ("a as uint8", lambda: bs.bsgemm_w8a8_int8(_i8(4, K).view(torch.uint8), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("another K", lambda: bs.bsgemm_w8a8_int8(_i8(4, 528), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("a_scale per group", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4, 4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("w_scale short", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N - 1))),
+    ("w_pre short", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4), _desc(), _i8(N * K - 1).view(torch.uint8), _f32(N))),
+    ("out fp32", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N), out=_f32(4, N))),
+    ("out of another shape", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N), out=_bf(4, N + 1))),
+    ("columns of a", lambda: bs.bsgemm_w8a8_int8(_i8(4, 2 * K)[:, ::2], _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("overlapping rows", lambda: bs.bsgemm_w8a8_int8(_i8(K + 64).as_strided((4, K), (16, 1)), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("host tensors", lambda: bs.bsgemm_w8a8_int8(_i8(4, K), _f32(4), _desc(), _i8(N * K).view(torch.uint8), _f32(N))),
+    ("grouped w_scale", lambda: bs.bsgemm_w8a8_int8_grouped(_i8(4, K), _f32(4), _i32(3), _desc(), _i8(2, N * K).view(torch.uint8), _f32(N))),
+    ("grouped offsets", lambda: bs.bsgemm_w8a8_int8_grouped(_i8(4, K), _f32(4), _i32(2), _desc(), _i8(2, N * K).view(torch.uint8), _f32(2, N))),
+    ("grouped rows", lambda: bs.bsgemm_w8a8_int8_grouped(_i8(4, K), _f32(4), _i32(3), _desc(), _i8(2, N * K).view(torch.uint8), _f32(2, N), rows=_f32(4))),
+    ("grouped on the host", lambda: bs.bsgemm_w8a8_int8_grouped(_i8(4, K), _f32(4), _i32(3), _desc(), _i8(2, N * K).view(torch.uint8), _f32(2, N))),
+    ("prelayout uint8", lambda: bs.prelayout_int8(_i8(16, 64).view(torch.uint8))),
+    ("prelayout on the host", lambda: bs.prelayout_int8(_i8(16, 64))),
+    ("prelayout 1-D", lambda: bs.prelayout_int8(_i8(64))),
+    ("no experts", lambda: bs.prelayout_int8_experts(_i8(0, 16, 64))),
+    ("quant fp32", lambda: bs.quant_int8_per_token(_f32(4, 64))),
+    ("quant codes", lambda: bs.quant_int8_per_token(_bf(4, 64), q=_bf(4, 64))),
+    ("quant on the host", lambda: bs.quant_int8_per_token(_bf(4, 64))),
+    ("norm gamma", lambda: bs.add_rms_quant_int8(_bf(4, 64), _bf(4, 64), _bf(65))),
+    ("norm residual", lambda: bs.add_rms_quant_int8(_bf(4, 64), _bf(3, 64), _bf(64))),
+    ("silu odd", lambda: bs.silu_mul_quant_int8(_bf(4, 65))),
+    ("silu rows", lambda: bs.silu_mul_quant_int8(_bf(4, 64), rows=_i32(2))),
+    ("dequant uint8", lambda: bs.dequant_int8(_i8(4, 64).view(torch.uint8), _f32(4))),
+    ("dequant scale", lambda: bs.dequant_int8(_i8(4, 64), _f32(5))),
+    ("route fp16", lambda: bs.moe_route(torch.zeros((4, 8), dtype=torch.float16), 2)),
+    ("route k", lambda: bs.moe_route(_f32(4, 8), 0)),
+    ("route k float", lambda: bs.moe_route(_f32(4, 8), 2.0)),
+    ("route bias", lambda: bs.moe_route(_f32(4, 8), 2, bias=_bf(8))),
+    ("route rows", lambda: bs.moe_route(_f32(4, 8), 2, rows=_i32(4))),
+    ("route ids", lambda: bs.moe_route(_f32(4, 8), 2, ids=_i32(4, 3))),
+    ("route on the host", lambda: bs.moe_route(_f32(4, 8), 2)),
+    ("route columns", lambda: bs.moe_route(_f32(4, 16)[:, ::2], 2)),
+    ("backward dweights", lambda: bs.moe_route_backward(_f32(4, 3), _f32(4, 8), _i32(4, 2))),
+    ("backward type", lambda: bs.moe_route_backward(_f32(4, 2), _f32(4, 8), _i32(4, 2), dlogits=_bf(4, 8))),
+    ("backward ids", lambda: bs.moe_route_backward(_f32(4, 2), _f32(4, 8), _f32(4, 2))),
+    ("backward on the host", lambda: bs.moe_route_backward(_f32(4, 2), _f32(4, 8), _i32(4, 2))),
+]
+
+
+@pytest.mark.parametrize("what,call", REFUSED, ids=[w for w, _ in REFUSED])
+def test_binding_refuses(blib, what, call):
+    with pytest.raises(ValueError):
+        call()
