@@ -150,23 +150,23 @@ BS_INLINE void xcd_tile(int b, int m_tiles, int n_tiles, int group_m, int& mt, i
 constexpr size_t kWsCounterBytes = 64 * 1024;
 constexpr int kWsMaxCounters = static_cast<int>(kWsCounterBytes / sizeof(int));
 
-// Split-K reduction of the last-arriving workgroup: sum[v] = the S fp32
-// partials base[b * stride + v * VSTRIDE] added in split order b = 0, 1, ...
-// (deterministic).  The partials were written with device-scope stores, so
+// Split-K reduction of the last-arriving workgroup: sum[v] = the S partials
+// base[b * stride + v * VSTRIDE] (fp32, or int32 where the sums are whole)
+// added in split order b = 0, 1, ... (deterministic).  The partials were written with device-scope stores, so
 // they are read with device-scope loads, which are served past the XCD's L2:
 // a round trip costs about a microsecond.  The loads of U splits are all
 // issued before any of them is added, so the reduction waits ceil(S / U)
 // round trips rather than one per split and value group.  Splits past S
 // re-read split S - 1 (valid memory) and are not added.
-template <int NV, int VSTRIDE, int U>
-BS_INLINE void sum_partials(float (&sum)[NV], const float* base, size_t stride, int S) {
+template <int NV, int VSTRIDE, int U, typename V>
+BS_INLINE void sum_partials(V (&sum)[NV], const V* base, size_t stride, int S) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) sum[v] = 0.0f;
+  for (int v = 0; v < NV; ++v) sum[v] = V(0);
   for (int b0 = 0; b0 < S; b0 += U) {
-    float x[U][NV];
+    V x[U][NV];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float* src = base + static_cast<size_t>(min(b0 + u, S - 1)) * stride;
+      const V* src = base + static_cast<size_t>(min(b0 + u, S - 1)) * stride;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         x[u][v] = __hip_atomic_load(src + v * VSTRIDE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -87,7 +87,7 @@ bool mx_desc_ok(const bs_wdesc* d, int N, int K) {
          d->total_bytes == off + scales;
 }
 bool i8_desc_ok(const bs_wdesc* d, int N, int K) {
-  const uint64_t bytes = static_cast<uint64_t>((N + 15) / 16) * ((K + 63) / 64) * 1024;
+  const uint64_t bytes = static_cast<uint64_t>((N + 15) / 16) * ((K + 127) / 128) * 2048;
   return d->magic == BS_WDESC_MAGIC && d->layout == BS_LAYOUT_INT8 && d->N == N && d->K == K &&
          d->codes_bytes == bytes && d->scales_offset == 0 && d->scales_bytes == 0 && d->total_bytes == bytes;
 }

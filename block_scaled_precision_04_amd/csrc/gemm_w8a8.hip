@@ -5,11 +5,18 @@
 //
 // The sum is exact: int32 holds K products of two 8-bit codes up to K = 131071.
 // So K may be cut anywhere (waves, groups, workgroups) without a change in the
-// result.  The weight is laid out in 16-row x 64-K fragment blocks of 1 KiB, rows
-// and K padded with zeros; activation bytes past K meet those zeros, so they may
-// be any valid bytes of the row.
+// result.  The weight is laid out in 16-row x 64-K fragment blocks of 1 KiB, N
+// padded with zeros to 16 and K to 128; activation bytes past K meet those zeros,
+// so they may be any valid bytes of the row.
 //
-// LDS-tiled kernel (k_w8a8_tile), fed through direct-to-LDS loads.
+// Two kernels.  Few rows: a weight stream (k_w8a8_stream), bound by HBM.  Many
+// rows: LDS-tiled (k_w8a8_tile), fed through direct-to-LDS loads.  Both have a
+// grouped form: the slots of the sorted (token, expert) pairs are cut into row
+// tiles expert by expert, and every workgroup finds its tile from the expert
+// offsets on the device, so the host never waits for them; the activation rows are
+// read through the sorted order (row gather in the loads), never copied.
+#include <cmath>
+
 #include "grouped.h"
 
 namespace {
@@ -23,10 +30,15 @@ struct W8A8Args {
   size_t w_stride;       // grouped: bytes from one expert's weight to the next
   uint16_t* c;
   int64_t ldc;
-  int M, N, K, KS;       // dense: rows; grouped: slots.  KS = ceil(K / 64)
+  int M, N, K, KS;       // dense: rows; grouped: slots.  KS: 64-K blocks of the weight, even
   const int* offsets;    // grouped: [E + 1]
   const int* rows;       // grouped: source row of each slot, or null
   int E, Ma;             // grouped: experts, rows of a
+  int tw, kw;            // stream: waves along N and along K
+  int rs;                // stream: activation rows staged per workgroup
+  int iters;             // stream: K runs per workgroup
+  int* slab;
+  int* counters;
 };
 
 // Source row of tile row i (slot r0 + i).
@@ -37,28 +49,233 @@ BS_INLINE int src_row(const W8A8Args& p, int slot) {
 
 BS_INLINE float scaled(int acc, float sa, float sw) { return static_cast<float>(acc) * sa * sw; }
 
+// ============================================================ few rows: stream
+// grid (column groups, row tiles, K splits): workgroup (x, y, z) computes
+// n-tiles [x*TW*T, (x+1)*TW*T) of 16 columns for the up to 16*MB rows of row
+// tile y (dense: all rows) over its run of `iters * KW * R` K blocks.  Wave (tw,
+// kw) owns T tiles over R blocks of each KW*R; the KW partial sums of a tile are
+// added through LDS, K splits through the workspace.  The activation slice (KW*R
+// blocks x rs rows x 64 B) is copied to LDS by direct loads, shared by the TW*T
+// tiles; the weights go straight to registers, all of a wave's loads at once.
+template <int MB, int T, int R, bool LOOP, bool GROUPED>
+__global__ __launch_bounds__(1024) void k_w8a8_stream(W8A8Args p) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ int last;
+  const int TW = p.tw, KW = p.kw, kSteps = KW * R;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tw = wave % TW, kw = wave / TW;
+  const int l = threadIdx.x & 63, g = l >> 4;
+  const int KS = p.KS, RS = p.rs, last_chunk = (p.K >> 4) - 1;
+  const int ntiles = (p.N + 15) >> 4;
+  const int tile0 = (blockIdx.x * TW + tw) * T;
+
+  int m0, nrows;
+  const uint8_t* w = p.w;
+  const float* wsc = p.wsc;
+  if constexpr (GROUPED) {
+    int e, r1;
+    if (!find_tile<16 * MB>(p.offsets, p.E, p.M, blockIdx.y, e, m0, r1)) return;
+    nrows = r1 - m0;
+    w += static_cast<size_t>(e) * p.w_stride;
+    wsc += static_cast<size_t>(e) * p.N;
+  } else {
+    m0 = 0;
+    nrows = RS;
+  }
+
+  // the owner's scales: its row of each row block, its four columns of each tile
+  const bool owner = kw == 0;
+  float sa[MB], sw[T][4];
+  if (owner) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      int src = m0 + min(16 * mb + (l & 15), nrows - 1);
+      if constexpr (GROUPED) src = src_row(p, src);
+      sa[mb] = p.as[src];
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sw[t][j] = wsc[min((tile0 + t) * 16 + 4 * g + j, p.N - 1)];
+  }
+
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+  const int a_instr = (kSteps * RS * 4 + 63) >> 6;
+  int* s_red = reinterpret_cast<int*>(lds);
+
+  v4i acc[T][MB];
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) acc[t][mb] = v4i{0, 0, 0, 0};
+
+  const int iters = LOOP ? p.iters : 1;   // (the loop costs register copies)
+  for (int it = 0; it < iters; ++it) {
+    const int wg_k0 = (blockIdx.z * iters + it) * kSteps;
+    if (LOOP && wg_k0 >= KS) break;
+    const int wg_steps = min(kSteps, KS - wg_k0);
+    const int ks0 = wg_k0 + kw * R;
+    const int klast = min(ks0 + R, KS) - 1;  // below ks0 for an idle wave
+    const int nsteps = klast - ks0 + 1;      // <= 0 for an idle wave
+    if (LOOP && it) __syncthreads();      // every wave is done with the slice
+    // chunk c of row i of block r sits at position (r*RS + i)*4 + swz4(i, c);
+    // positions past the slice, and chunks past K, re-read valid bytes (the
+    // weight is zero there)
+    for (int k = wave; k < a_instr; k += TW * KW) {
+      const int q = k * 64 + l;
+      const int ri = q >> 2;
+      const int r = min(ri / RS, wg_steps - 1);
+      const int ii = ri % RS;
+      int row = m0 + min(ii, nrows - 1);
+      if constexpr (GROUPED) row = src_row(p, row);
+      dma16(lds0 + k * 1024, p.a,
+            static_cast<uint32_t>(row) * p.lda +
+                static_cast<uint32_t>(min((wg_k0 + r) * 4 + swz4(ii, q & 3), last_chunk) * 16));
+    }
+    v4i wf[T][R];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const size_t tile = static_cast<size_t>(min(tile0 + t, ntiles - 1));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const size_t ks = max(min(ks0 + r, klast), 0);
+        const uint4 x = ld_stream16(reinterpret_cast<const uint4*>(w + (tile * KS + ks) * 1024 + l * 16));
+        wf[t][r] = v4i{(int)x.x, (int)x.y, (int)x.z, (int)x.w};
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<T * R>();  // this wave's activation loads have landed
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= nsteps) break;
+      v4i af[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int rc = min(16 * mb + (l & 15), RS - 1);
+        af[mb] = *reinterpret_cast<const v4i*>(lds + ((kw * R + r) * RS + rc) * 64 + (swz4(rc, g) << 4));
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+          acc[t][mb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[t][r], af[mb], acc[t][mb], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  if (KW > 1) {   // the KW partials of a tile
+    constexpr int kPer = T * MB * 4;
+    __syncthreads();
+    if (kw > 0) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s_red[(((kw - 1) * TW + tw) * kPer + (t * MB + mb) * 4 + j) * 64 + l] = acc[t][mb][j];
+    }
+    __syncthreads();
+    if (kw == 0)
+      for (int u = 1; u < KW; ++u)
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[t][mb][j] += s_red[(((u - 1) * TW + tw) * kPer + (t * MB + mb) * 4 + j) * 64 + l];
+  }
+  const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.c) % 8 == 0;
+  auto store = [&](int t, int mb, v4i v) {
+    const int i = 16 * mb + (l & 15), n = (tile0 + t) * 16 + 4 * g;
+    if (i >= nrows || n >= p.N) return;
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = scaled(v[j], sa[mb], sw[t][j]);
+    const uint2 o{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])};
+    uint16_t* dst = p.c + (m0 + i) * p.ldc + n;
+    if (wide && n + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(dst) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < p.N) dst[j] = static_cast<uint16_t>((j < 2 ? o.x : o.y) >> (16 * (j & 1)));
+    }
+  };
+  const int S = gridDim.z;
+  if (GROUPED || S == 1) {
+    if (owner)
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) store(t, mb, acc[t][mb]);
+    return;
+  }
+  // K splits: partials in fragment order, device-scope, added by the last
+  // workgroup of the tile; it leaves its counter at zero.
+  const int tg = blockIdx.y * gridDim.x + blockIdx.x;
+  auto frag = [&](int sp, int t, int mb) {
+    const size_t f =
+        ((((static_cast<size_t>(sp) * gridDim.y * gridDim.x) + tg) * TW + tw) * T + t) * MB + mb;
+    return p.slab + f * 256 + l;
+  };
+  if (owner)
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        int* dst = frag(blockIdx.z, t, mb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __hip_atomic_store(dst + j * 64, acc[t][mb][j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  asm volatile("" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(&p.counters[tg], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == S - 1;
+  __syncthreads();
+  if (!last || !owner) return;
+  constexpr int kNV = T * MB * 4;
+  constexpr int kU = kNV >= 32 ? 2 : (kNV >= 16 ? 4 : 8);
+  int sum[kNV];
+  sum_partials<kNV, 64, kU>(sum, frag(0, 0, 0), static_cast<size_t>(gridDim.y) * gridDim.x * (TW * T * MB * 256), S);
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int v = (t * MB + mb) * 4;
+      store(t, mb, v4i{sum[v], sum[v + 1], sum[v + 2], sum[v + 3]});
+    }
+  if (threadIdx.x == 0) __hip_atomic_store(&p.counters[tg], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ========================================================= many rows: LDS tiles
 // A workgroup computes a BM x BN tile with WM x WN waves, each (BM/WM) x
 // (BN/WN) as 32x32 sub-tiles; first MFMA operand the weight (rows = n), second
 // the activation, so a lane holds four consecutive n of one m.
 //
-// K advances in 64-wide steps.  A step's activation codes (BM x 64 B, chunks
-// swizzled by swz4) and weight codes (BN/16 fragment blocks of 1 KiB, as they
-// are) go global -> LDS by direct loads into one of STAGES buffers, STAGES - 1
+// K advances in steps of SUB blocks of 64.  A block's activation codes (BM x 64 B,
+// chunks swizzled by swz4) and weight codes (BN/16 fragment blocks of 1 KiB, as
+// they are) go global -> LDS by direct loads into one of STAGES buffers, STAGES - 1
 // steps ahead.  The steps of a turn round the stages are unrolled, so the stage
 // is a constant of the code.
 //
 // KG > 1: that many groups of WM x WN waves share the tile, each over every
 // KG-th step with buffers of its own, and their partial sums are added through
-// LDS.  TAIL: K is no multiple of 64.
-template <int BM, int BN, int WM, int WN, int KG, int STAGES>
+// LDS.  TAIL: K is no multiple of 128.
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB>
 struct TileCfg {
+  static_assert(STAGES >= 2 && STAGES <= 4 && (SUB == 1 || SUB == 2), "the K loop");
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;   // of a group
   static constexpr int kTM = BM / WM / 32, kTN = BN / WN / 32;
-  static constexpr int kA = BM * 64, kB = BN * 64, kStage = kA + kB;
-  static constexpr int kAIters = kA / (kThreads * 16), kBIters = kB / (kThreads * 16);
-  static constexpr int kDma = kAIters + kBIters;
-  static constexpr int kDmaFirst = (kDma + 1) / 2;      // of them, in the half step that frees the stage
+  static constexpr int kA = BM * 64, kB = BN * 64, kBlock = kA + kB, kStage = SUB * kBlock;
+  static constexpr int kAIters = kA / (kThreads * 16), kBIters = kB / (kThreads * 16);   // loads per 64 of K
+  static constexpr int kDma = SUB * (kAIters + kBIters), kHalves = 2 * SUB;
+  static constexpr int kDmaFirst = (kDma + kHalves - 1) / kHalves;   // of them, in the half that frees the stage
   static_assert(kA % (kThreads * 16) == 0 && kB % (kThreads * 16) == 0, "");
   static constexpr int kGroup = STAGES * kStage;         // LDS of a group
   static constexpr int kRed = (KG - 1) * BM * BN * 4;    // the other groups' partial tiles
@@ -69,9 +286,9 @@ struct TileCfg {
   static constexpr int kLds = kMain + kScales;
 };
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC, bool GROUPED, bool TAIL>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB, int OCC, bool GROUPED, bool TAIL>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p, int group_m) {
-  using C = TileCfg<BM, BN, WM, WN, KG, STAGES>;
+  using C = TileCfg<BM, BN, WM, WN, KG, STAGES, SUB>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
   const int tid = threadIdx.x;
   const int wg_wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
@@ -79,8 +296,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   const int wm = wave / WN, wn = wave % WN;
   const int N = p.N, KS = p.KS, NT = (N + 15) >> 4;
   const int n_tiles = (N + BN - 1) / BN;
-  // this group's steps: KG * i + kg for i < n_steps
-  const int n_steps = (KS - kg + KG - 1) / KG, n_turns = (KS + KG - 1) / KG;
+  // this group's steps of SUB blocks of K: KG * i + kg for i < n_steps
+  const int SS = KS / SUB;
+  const int n_steps = (SS - kg + KG - 1) / KG, n_turns = (SS + KG - 1) / KG;
 
   int m0, nrows, nt;
   const uint8_t* w = p.w;
@@ -123,16 +341,18 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   for (int i = 0; i < C::kBIters; ++i)
     boff[i] = static_cast<uint32_t>(min(nt0 + i * C::kWaves + wave, NT - 1) - nt0) * static_cast<uint32_t>(KS) * 1024u +
               static_cast<uint32_t>(l * 16);
-  // the i-th load of step ks into stage st
-  auto dma_one = [&](int i, int ks, int st) {
-    const uint32_t base = lds0 + st * C::kStage;
-    if (i < C::kAIters) {
-      const uint32_t dst = base + (i * C::kWaves + wave) * 1024;
-      if constexpr (TAIL) dma16(dst, a, min(aoff[i] + static_cast<uint32_t>(ks) * 64u, aend[i]));
-      else dma16(dst, a + static_cast<size_t>(ks) * 64, aoff[i]);
+  // the i-th load of step ss into stage st
+  auto dma_one = [&](int i, int ss, int st) {
+    const int sub = i / (C::kAIters + C::kBIters), j = i % (C::kAIters + C::kBIters);
+    const int ks = ss * SUB + sub;
+    const uint32_t base = lds0 + st * C::kStage + sub * C::kBlock;
+    if (j < C::kAIters) {
+      const uint32_t dst = base + (j * C::kWaves + wave) * 1024;
+      if constexpr (TAIL) dma16(dst, a, min(aoff[j] + static_cast<uint32_t>(ks) * 64u, aend[j]));
+      else dma16(dst, a + static_cast<size_t>(ks) * 64, aoff[j]);
     } else {
-      dma16(base + C::kA + ((i - C::kAIters) * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024,
-            boff[i - C::kAIters]);
+      dma16(base + C::kA + ((j - C::kAIters) * C::kWaves + wave) * 1024, w + static_cast<size_t>(ks) * 1024,
+            boff[j - C::kAIters]);
     }
   };
 
@@ -156,25 +376,29 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
     v4i b[C::kTN], a[C::kTM];
   };
   constexpr int kPieces = C::kTN + C::kTM;
-  // LDS read piece i of half hh of stage st: weight 0, the activations, the other weights
-  auto piece = [&](int st, int hh, Frag& f, int i) {
-    const uint8_t* base = glds + st * C::kStage;
+  // LDS read piece i of half h of stage st: weight 0, the activations, the other weights
+  auto piece = [&](int st, int h, Frag& f, int i) {
+    const uint8_t* base = glds + st * C::kStage + (h >> 1) * C::kBlock;
     if (i == 0 || i > C::kTM) {
       const int t = i == 0 ? 0 : i - C::kTM;
-      f.b[t] = *reinterpret_cast<const v4i*>(base + bbase + t * 2048 + hh * 512);
+      f.b[t] = *reinterpret_cast<const v4i*>(base + bbase + t * 2048 + (h & 1) * 512);
     } else {
-      f.a[i - 1] = *reinterpret_cast<const v4i*>(base + abase[hh] + (i - 1) * 2048);
+      f.a[i - 1] = *reinterpret_cast<const v4i*>(base + abase[h & 1] + (i - 1) * 2048);
     }
   };
-  // MFMAs of half HH of the step in stage U.  Between them: the LDS reads of the
-  // next half (rf) and half of a step's loads (HH 0: the rest of step s + STAGES
-  // - 1's; HH 1: the first of step s + STAGES's, whose stage has just become free).
+  // MFMAs of half H of the step in stage U.  Between them: the LDS reads of the
+  // next half (rf) and a share of a step's loads (the last half: the first of step
+  // s + STAGES's, whose stage has just become free; the others: the rest of step
+  // s + STAGES - 1's).
   auto half = [&](auto uu, auto hh, const Frag& f, Frag& rf, int dks) {
-    constexpr int U = decltype(uu)::value, HH = decltype(hh)::value;
-    constexpr int kRead = HH == 0 ? U : (U + 1) % STAGES;
+    constexpr int U = decltype(uu)::value, H = decltype(hh)::value;
+    constexpr bool kLast = H == C::kHalves - 1;
+    constexpr int kRead = kLast ? (U + 1) % STAGES : U;
     constexpr int kN = C::kTN * C::kTM;
-    constexpr int d0 = HH ? 0 : C::kDmaFirst, d1 = HH ? C::kDmaFirst : C::kDma;
-    constexpr int kFill = HH ? U : (U + STAGES - 1) % STAGES;
+    constexpr int kRest = C::kDma - C::kDmaFirst;
+    constexpr int d0 = kLast ? 0 : C::kDmaFirst + H * kRest / (C::kHalves - 1);
+    constexpr int d1 = kLast ? C::kDmaFirst : C::kDmaFirst + (H + 1) * kRest / (C::kHalves - 1);
+    constexpr int kFill = kLast ? U : (U + STAGES - 1) % STAGES;
 #pragma unroll
     for (int n = 0; n < kN || n < kPieces; ++n) {
       if (n < kN) {
@@ -182,7 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[i], f.a[j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (n < kPieces) piece(kRead, 1 - HH, rf, n);
+      if (n < kPieces) piece(kRead, kLast ? 0 : H + 1, rf, n);
       // the loads, spread evenly over the half's MFMAs
 #pragma unroll
       for (int d = d0; d < d1; ++d)
@@ -191,13 +415,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
     }
   };
 
-  // Step s: first half; this wave's loads of step s+1 have landed and its LDS
-  // reads are done; barrier (s+1 published, the stage of s free); second half,
-  // which reads s+1's first fragments.  So a stage is filled again right behind
+  // Step s: all halves but the last; this wave's loads of step s+1 have landed and
+  // its LDS reads are done; barrier (s+1 published, the stage of s free); the last
+  // half, which reads s+1's first fragments.  So a stage is filled again right behind
   // its last reads and waited for only where it is read, STAGES - 1 steps later.
   // Steps past the end re-load the last one (never used, or the same bytes).
   Frag f0, f1;
-  auto step_of = [&](int ls) { return min(KG * min(ls, n_steps - 1) + kg, KS - 1); };
+  auto step_of = [&](int ls) { return min(KG * min(ls, n_steps - 1) + kg, SS - 1); };
   {
     // scales: rows, then columns, 64 a load, straight to their place in LDS
     const uint32_t sbase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + C::kMain;
@@ -233,21 +457,27 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   // the group's ls-th step, in stage U (live: it exists)
   auto step = [&](auto uu, int ls, bool live) {
     if (KG == 1 || live) {
-      half(uu, Int<0>{}, f0, f1, step_of(ls + STAGES - 1));
+      const int next = step_of(ls + STAGES - 1);
+      half(uu, Int<0>{}, f0, f1, next);
+      if constexpr (SUB > 1) {
+        half(uu, Int<1>{}, f1, f0, next);
+        half(uu, Int<2>{}, f0, f1, next);
+      }
       wait_vm<(STAGES - 2) * C::kDma>();
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     if (KG > 1 && !live) return;
-    half(uu, Int<1>{}, f1, f0, step_of(ls + STAGES));
+    half(uu, Int<C::kHalves - 1>{}, f1, f0, step_of(ls + STAGES));
   };
   // (with one group, steps past the end are skipped; several groups meet at
   // every barrier, so those run it empty)
   for (int ls = 0; ls < n_turns; ls += STAGES) {
     step(Int<0>{}, ls, ls < n_steps);
     if (ls + 1 < n_turns) step(Int<1>{}, ls + 1, ls + 1 < n_steps);
-    if (ls + 2 < n_turns) step(Int<2>{}, ls + 2, ls + 2 < n_steps);
+    if constexpr (STAGES > 2)
+      if (ls + 2 < n_turns) step(Int<2>{}, ls + 2, ls + 2 < n_steps);
     if constexpr (STAGES > 3)
       if (ls + 3 < n_turns) step(Int<3>{}, ls + 3, ls + 3 < n_steps);
   }
@@ -336,22 +566,204 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
 }
 
 // ---------------------------------------------------------------- host side
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC, bool GROUPED>
-int launch_tile(const W8A8Args& p, int64_t wgs, hipStream_t st) {
-  if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
-  const dim3 grid(static_cast<uint32_t>(wgs)), block(64 * WM * WN * KG);
-  if (p.K % 64 == 0) k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, OCC, GROUPED, false><<<grid, block, 0, st>>>(p, 4);
-  else k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, OCC, GROUPED, true><<<grid, block, 0, st>>>(p, 4);
+constexpr size_t kMaxStreamLds = 160 * 1024 - 256;
+constexpr int kMaxSplits = 65535;   // grid z
+
+struct StreamCfg {
+  int mb, tw, kw, t, r;                  // row blocks, waves, tiles and K blocks a wave
+  int rs, groups, mtiles, s, iters;      // rows staged, the grid, K runs a workgroup
+};
+size_t stream_lds(const StreamCfg& d) {
+  const size_t slice = (static_cast<size_t>(d.kw) * d.r * d.rs * 4 + 63) / 64 * 1024;
+  const size_t red = static_cast<size_t>(d.kw - 1) * d.tw * d.t * d.mb * 4 * 64 * sizeof(int);
+  return std::max(slice, red);
+}
+size_t stream_slab(const StreamCfg& d) {
+  return static_cast<size_t>(d.s) * d.mtiles * d.groups * d.tw * d.t * d.mb * 1024;
+}
+
+template <int MB, int T, int R, bool LOOP, bool GROUPED>
+int launch_stream(const StreamCfg& d, W8A8Args& p, hipStream_t st) {
+  const size_t lds = stream_lds(d);
+  if (lds > kMaxStreamLds || d.tw * d.kw > 16 || d.mtiles > 65535 || d.s > kMaxSplits) return BS_ERR_SHAPE;
+  p.tw = d.tw;
+  p.kw = d.kw;
+  p.rs = d.rs;
+  p.iters = d.iters;
+  auto* fn = &k_w8a8_stream<MB, T, R, LOOP, GROUPED>;
+  static const hipError_t attr =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          static_cast<int>(kMaxStreamLds));
+  if (attr != hipSuccess) return BS_ERR_LAUNCH;
+  fn<<<dim3(d.groups, d.mtiles, d.s), d.tw * d.kw * 64, lds, st>>>(p);
   return bs_launch_status();
 }
 
-int64_t tiles(int M, int N, int bm, int bn) {
-  return static_cast<int64_t>((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+// rows M as blocks of 16, columns and K cut as (tw, kw, t, r, iters) says
+StreamCfg stream_cfg(int M, int N, int KS, int mb, int tw, int kw, int t, int r, int iters) {
+  const int run = kw * r * iters;
+  return StreamCfg{mb, tw, kw, t, r, M, ((N + 15) / 16 + tw * t - 1) / (tw * t), 1, (KS + run - 1) / run, iters};
+}
+
+// The dense stream's cuts, from sweeps over N = 64 .. 34816 and K = 128 .. 17408
+// with weights pooled past the last-level cache.
+// Up to 16 rows (the choice is 2% behind the best of 22 cuts in the mean of 300
+// sizes, at worst 20%): one workgroup covers a K of up to 128 blocks (K = 8192)
+// with waves of eight blocks, so nothing goes through the workspace (8 rows N =
+// 17408 K = 5120 17.3 us, 5.2 TB/s; in two splits of five waves 19.4); two
+// column tiles a wave where 257 to 512 of them would leave a part of a second
+// round (N = K = 5120 7.6 against 8.3); short K in waves of four.  Longer K, and
+// 9 to 16 rows of many columns, whose slice would fill a CU's LDS alone, in runs
+// of four to six waves.
+// 17 to 64 rows: K in runs of a loop, so that about 256 to 512 workgroups stay.
+StreamCfg dense_stream_cfg(int M, int N, int KS) {
+  const int nt = (N + 15) / 16;
+  auto cut = [&](int tw, int t, int r, int kw_max) {
+    const int s = (KS + r * kw_max - 1) / (r * kw_max);
+    return stream_cfg(M, N, KS, 1, tw, (KS + s * r - 1) / (s * r), t, r, 1);
+  };
+  if (M <= 16) {
+    if (KS <= 8) return cut(2, 1, 4, 4);
+    if (KS <= 16) return cut(1, 1, 4, 4);
+    if (KS <= 128 && !(M > 8 && nt > 512) && !(KS > 80 && nt <= 32)) return cut(1, nt > 256 && nt <= 512 ? 2 : 1, 8, 16);
+    if (nt <= 32) return cut(1, 1, 8, 5);
+    return M > 8 && nt >= 256 ? cut(4, 1, 8, 4) : cut(2, 1, 8, 6);
+  }
+  auto loop = [&](int tw, int r, int kw, int target) {
+    kw = std::min(kw, (KS + r - 1) / r);
+    const int runs = (KS + kw * r - 1) / (kw * r), groups = (nt + tw - 1) / tw;
+    const int s = std::max(1, std::min(runs, target / groups));
+    return stream_cfg(M, N, KS, M <= 32 ? 2 : 4, tw, kw, 1, r, (runs + s - 1) / s);
+  };
+  if (M <= 32) {
+    if (KS <= 2) return loop(4, 4, 4, 256);
+    if (KS <= 8) return loop(2, 4, 2, 256);
+    if (KS <= 32) return nt <= 128 ? loop(1, 4, 8, 256) : loop(2, 4, 4, 256);
+    return nt <= 64 ? loop(2, 4, 4, 512) : (nt <= 512 ? loop(2, 8, 4, 256) : loop(4, 8, 2, 1024));
+  }
+  return nt <= 64 ? loop(2, 4, 4, 256) : (nt <= 512 ? loop(4, 4, 4, 256) : loop(8, 8, 1, 512));
+}
+
+// Up to 32 rows, and up to 64 of K > 2048 where the tiles' columns are few or K
+// is long (64 rows: N = 1024 K = 17408 13.6 us, tiles 42; N = K = 5120 13.4
+// against 16.8; N = 17408 K = 5120 29.5 against 28.7, left to the tiles).  A K
+// split has a counter for every column group and a grid layer for every run.
+bool use_stream(int M, int N, int KS) {
+  if (M > 32 && (M > 64 || KS <= 32 || (N > 8192 && KS < 192))) return false;
+  const StreamCfg d = dense_stream_cfg(M, N, KS);
+  return d.s == 1 || (d.s <= kMaxSplits && d.groups * d.mtiles <= kWsMaxCounters);
+}
+
+int run_dense_stream(W8A8Args& p, void* ws, hipStream_t st) {
+  const StreamCfg d = dense_stream_cfg(p.M, p.N, p.KS);
+  if (d.s > 1) {
+    p.counters = static_cast<int*>(ws);
+    p.slab = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
+  }
+#define BS_STREAM(MB_, R_) \
+  (d.iters > 1 ? launch_stream<MB_, 1, R_, true, false>(d, p, st) : launch_stream<MB_, 1, R_, false, false>(d, p, st))
+  if (d.mb == 1) {
+    if (d.r == 4) return launch_stream<1, 1, 4, false, false>(d, p, st);
+    return d.t == 2 ? launch_stream<1, 2, 8, false, false>(d, p, st) : launch_stream<1, 1, 8, false, false>(d, p, st);
+  }
+  if (d.mb == 2) return d.r == 4 ? BS_STREAM(2, 4) : BS_STREAM(2, 8);
+  return d.r == 4 ? BS_STREAM(4, 4) : BS_STREAM(4, 8);
+#undef BS_STREAM
+}
+
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB, int OCC, bool GROUPED>
+int launch_tile(const W8A8Args& p, int64_t wgs, hipStream_t st) {
+  if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
+  const dim3 grid(static_cast<uint32_t>(wgs)), block(64 * WM * WN * KG);
+  if (p.K % 128 == 0) k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, false><<<grid, block, 0, st>>>(p, 4);
+  else k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, true><<<grid, block, 0, st>>>(p, 4);
+  return bs_launch_status();
+}
+
+// The dense tile shapes and what a launch of each takes, in us: with x = tiles
+// / 256 (one per CU) and R = ceil(x) rounds,
+//   t = start + R * (round + steps * step) + x * steps * load,  steps of 128 of K
+// fitted over 14 row counts from 65 to 4096 at twelve N x K, N = 512 .. 34816 and
+// K = 256 .. 17408, weights pooled past the last-level cache: by least squares,
+// then moved to the least loss by the choice (1.0% behind the best shape in the
+// mean of 168 sizes, at worst 12%).
+struct TileShape {
+  int bm, bn;
+  float start, round, step, load;
+};
+constexpr TileShape kTiles[] = {
+    {256, 256, 0.000f, 6.713f, 1.080f, 0.687f},  // 8 waves of 64 x 128
+    {128, 256, 1.266f, 2.716f, 0.918f, 0.128f},  // 4 waves of 64 x 128, two workgroups a CU
+    {128, 256, 0.000f, 3.739f, 0.859f, 0.188f},  // 8 waves of 64 x 64
+    {128, 128, 0.898f, 2.051f, 0.601f, 0.026f},  // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 2.688f, 0.450f, 0.435f, 0.060f},   // 4 waves of 64 x 32, three workgroups a CU
+    {64, 128, 2.483f, 3.453f, 0.371f, 0.000f},   // 2 K groups of 2 waves of 64 x 64
+    {64, 64, 2.096f, 0.434f, 0.216f, 0.069f},    // 4 waves of 32 x 32, K steps of 128, two workgroups a CU
+};
+constexpr int kShapes = sizeof(kTiles) / sizeof(kTiles[0]);
+int64_t tiles_of(int i, int M, int N) {
+  const TileShape& t = kTiles[i];
+  return static_cast<int64_t>((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+float tile_cost(int i, int M, int N, int steps) {
+  const TileShape& t = kTiles[i];
+  const float x = static_cast<float>(tiles_of(i, M, N)) / 256.0f;
+  return t.start + std::ceil(x) * (t.round + steps * t.step) + x * steps * t.load;
+}
+int best_tile(int M, int N, int steps) {
+  int best = 0;
+  for (int i = 1; i < kShapes; ++i)
+    if (tile_cost(i, M, N, steps) < tile_cost(best, M, N, steps)) best = i;
+  return best;
+}
+
+// columns [n0, n1) of the problem as tiles of shape i; n0 is a multiple of 16
+int run_tiles(int i, const W8A8Args& q, int n0, int n1, hipStream_t st) {
+  W8A8Args p = q;
+  p.w += static_cast<size_t>(n0 / 16) * p.KS * 1024;
+  p.wsc += n0;
+  p.c += n0;
+  p.N = n1 - n0;
+  const int64_t wgs = tiles_of(i, p.M, p.N);
+  switch (i) {
+    case 0: return launch_tile<256, 256, 4, 2, 1, 4, 1, 1, false>(p, wgs, st);
+    case 1: return launch_tile<128, 256, 2, 2, 1, 3, 1, 2, false>(p, wgs, st);
+    case 2: return launch_tile<128, 256, 2, 4, 1, 4, 1, 1, false>(p, wgs, st);
+    case 3: return launch_tile<128, 128, 2, 2, 1, 4, 1, 2, false>(p, wgs, st);
+    case 4: return launch_tile<64, 128, 1, 4, 1, 4, 1, 3, false>(p, wgs, st);
+    case 5: return launch_tile<64, 128, 1, 2, 2, 4, 1, 1, false>(p, wgs, st);
+    default: return launch_tile<64, 64, 2, 2, 1, 4, 2, 2, false>(p, wgs, st);
+  }
+}
+
+// One shape for all columns; or, where the large tiles would end in a partial
+// round, large tiles over as many columns as whole rounds take and the rest as
+// the shape that is quickest there (the second launch costs about 1 us more).
+int run_dense_tile(const W8A8Args& p, hipStream_t st) {
+  const int steps = p.KS / 2, b = best_tile(p.M, p.N, steps);
+  const int64_t mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
+  const int64_t rounds = mt * nt / 256;
+  if (rounds >= 1) {
+    const int n1 = static_cast<int>(rounds * 256 / mt * 256);   // < N unless the rounds are whole
+    if (n1 > 0 && n1 < p.N) {
+      const int r = best_tile(p.M, p.N - n1, steps);
+      if (tile_cost(0, p.M, n1, steps) + tile_cost(r, p.M, p.N - n1, steps) + 1.0f < tile_cost(b, p.M, p.N, steps)) {
+        const int rc = run_tiles(0, p, 0, n1, st);
+        return rc != BS_OK ? rc : run_tiles(r, p, n1, p.N, st);
+      }
+    }
+  }
+  return run_tiles(b, p, 0, p.N, st);
 }
 
 }  // namespace
 
-size_t bs_w8a8_workspace(int M, int N, int K) { return 0; }
+size_t bs_w8a8_workspace(int M, int N, int K) {
+  const int KS = (K + 127) / 128 * 2;
+  if (!use_stream(M, N, KS)) return 0;
+  const StreamCfg d = dense_stream_cfg(M, N, KS);
+  return d.s > 1 ? kWsCounterBytes + stream_slab(d) : 0;
+}
 
 int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t* w, const float* wsc, uint16_t* c,
                    int64_t ldc, int M, int N, int K, void* ws, hipStream_t st) {
@@ -366,9 +778,8 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
   p.M = M;
   p.N = N;
   p.K = K;
-  p.KS = (K + 63) / 64;
-  if (tiles(M, N, 128, 128) >= 256) return launch_tile<128, 128, 2, 2, 1, 4, 2, false>(p, tiles(M, N, 128, 128), st);
-  return launch_tile<64, 64, 2, 2, 1, 4, 4, false>(p, tiles(M, N, 64, 64), st);
+  p.KS = (K + 127) / 128 * 2;
+  return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, st);
 }
 
 int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const int* offsets, const int* rows,
@@ -386,13 +797,13 @@ int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const
   p.M = S;
   p.N = N;
   p.K = K;
-  p.KS = (K + 63) / 64;
+  p.KS = (K + 127) / 128 * 2;
   p.offsets = offsets;
   p.rows = rows;
   p.E = E;
   p.Ma = Ma;
   if (S / E > 64)
-    return launch_tile<128, 128, 2, 2, 1, 4, 2, true>(
+    return launch_tile<128, 128, 2, 2, 1, 4, 1, 2, true>(
         p, static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 127) / 128), st);
-  return launch_tile<64, 64, 2, 2, 1, 4, 4, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 63) / 64), st);
+  return launch_tile<64, 64, 2, 2, 1, 4, 1, 4, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 63) / 64), st);
 }

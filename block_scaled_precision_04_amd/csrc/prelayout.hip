@@ -13,7 +13,8 @@
 //              then e8m0 scales, one dword per lane per (nt, group of four
 //              steps), byte ks%4, pad 0x7F.
 //   int8       1 KiB per (nt, 64-wide step): 16 bytes per lane, K = 64*ks +
-//              16*(l/16) .. +15; rows and K past the end are zeros.
+//              16*(l/16) .. +15; rows up to a multiple of 16 and K up to one
+//              of 128 are zeros.
 // Every kernel moves 16-byte chunks except the scale gather (4 bytes).
 #include "common.h"
 
@@ -126,7 +127,7 @@ bool shape_ok(int N, int K) { return N >= 16 && N % 16 == 0 && K >= 128 && K % 1
 
 // (products of two 8-bit codes, summed in int32 without overflow: K < 2^17)
 bool i8_shape_ok(int N, int K) { return N >= 1 && N <= (1 << 24) && K >= 16 && K % 16 == 0 && K < (1 << 17); }
-uint64_t i8_bytes(int N, int K) { return static_cast<uint64_t>((N + 15) / 16) * ((K + 63) / 64) * 1024; }
+uint64_t i8_bytes(int N, int K) { return static_cast<uint64_t>((N + 15) / 16) * ((K + 127) / 128) * 2048; }
 
 uint64_t mx_codes_bytes(int N, int K) { return static_cast<uint64_t>(N) * K / 2; }
 uint64_t mx_scale_bytes(int N, int K) { return static_cast<uint64_t>(N / 16) * ((K / 128 + 3) / 4) * 256; }
@@ -227,7 +228,7 @@ BS_API int bs_prelayout_int8(const void* w, void* out, size_t out_bytes, int N, 
   const uint64_t bytes = i8_bytes(N, K);
   BS_CHECK(out_bytes >= bytes, BS_ERR_ARG);
   k_i8_pre<<<blocks_for(bytes / 16), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
-      static_cast<const uint4*>(w), static_cast<uint4*>(out), bytes / 16, (K + 63) / 64, N, K / 16, false);
+      static_cast<const uint4*>(w), static_cast<uint4*>(out), bytes / 16, (K + 127) / 128 * 2, N, K / 16, false);
   const int st = bs_launch_status();
   if (st != BS_OK) return st;
   *desc = bs_wdesc{BS_WDESC_MAGIC, BS_LAYOUT_INT8, N, K, bytes, 0, 0, bytes};
@@ -240,7 +241,7 @@ BS_API int bs_unprelayout_int8(const bs_wdesc* d, const void* pre, void* w, bs_s
   BS_CHECK(bs_aligned(w, 16) && bs_aligned(pre, 256), BS_ERR_ALIGN);
   const size_t nchunks = i8_bytes(d->N, d->K) / 16;
   k_i8_pre<<<blocks_for(nchunks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
-      static_cast<const uint4*>(pre), static_cast<uint4*>(w), nchunks, (d->K + 63) / 64, d->N, d->K / 16, true);
+      static_cast<const uint4*>(pre), static_cast<uint4*>(w), nchunks, (d->K + 127) / 128 * 2, d->N, d->K / 16, true);
   return bs_launch_status();
 }
 

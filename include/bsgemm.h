@@ -88,8 +88,8 @@ BS_API int bs_version(void);
  *               of its row and K-block l/16 for those four steps (byte = ks%4;
  *               unused bytes of a final partial dword are 0x7F).
  *   int8:       K steps of 64: per (nt, ks) 1 KiB, lane l's 16 bytes
- *               W[n][64ks + 16(l/16) .. +16] at offset 16*l; rows past N and
- *               bytes past K are zeros.
+ *               W[n][64ks + 16(l/16) .. +16] at offset 16*l; rows are padded
+ *               to a multiple of 16 and K to one of 128 with zeros.
  */
 enum {
   BS_LAYOUT_FP8_BLOCK = 0x38423631, /* e4m3 codes, 16x128 fragment order   */

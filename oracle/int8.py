@@ -68,9 +68,9 @@ def gemm(a, a_scale, w, w_scale):
 
 
 def prelayout(w):
-    """int8 [N, K] -> the bytes of the fragment order, rows and K padded with zeros."""
+    """int8 [N, K] -> the bytes of the fragment order, rows padded to 16 and K to 128 with zeros."""
     N, K = w.shape
-    nt, ks = (N + 15) // 16, (K + 63) // 64
+    nt, ks = (N + 15) // 16, (K + 127) // 128 * 2
     full = np.zeros((nt * 16, ks * 64), np.int8)
     full[:N, :K] = w
     # [tile, row, step, chunk, byte] -> [tile, step, chunk, row, byte]

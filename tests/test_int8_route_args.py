@@ -27,13 +27,13 @@ def blib():
 
 
 def _desc(n=N, k=K):
-    b = (n + 15) // 16 * ((k + 63) // 64) * 1024
+    b = (n + 15) // 16 * ((k + 127) // 128) * 2048
     return WDesc(BS_WDESC_MAGIC, BS_LAYOUT_INT8, n, k, b, 0, 0, b)
 
 
 def test_prelayout(blib):
     size = blib.bs_prelayout_int8_bytes
-    assert size(16, 64) == 1024 and size(17, 80) == 4096 and size(1, 16) == 1024
+    assert size(16, 64) == 2048 and size(17, 144) == 8192 and size(1, 16) == 2048
     assert size(0, 64) == 0 and size(16, 0) == 0 and size(16, 24) == 0 and size(16, 1 << 17) == 0
     assert size(16, (1 << 17) - 16) == 2048 * 1024 and size((1 << 24) + 1, 16) == 0
     d = WDesc()

@@ -99,7 +99,7 @@ def test_prelayout_order():
     for N, K in ((16, 64), (21, 80), (1, 16), (33, 256)):
         w = g.integers(-128, 128, (N, K)).astype(np.int8)
         out = int8.prelayout(w).view(np.int8)
-        ks = -(-K // 64)
+        ks = -(-K // 128) * 2
         assert out.size == -(-N // 16) * ks * 1024
         for i in g.integers(0, out.size, 500):
             block, lane, byte = i // 1024, i % 1024 // 16, i % 16
