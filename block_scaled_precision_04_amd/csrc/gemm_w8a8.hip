@@ -782,6 +782,22 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
   return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, st);
 }
 
+// Row tiles by S / E, the rows an expert would have if they were spread evenly
+// (swept at 256, 128, 64, 32, 16 and 8 experts, S / E from 1/32 to 2048, weights
+// pooled past the last-level cache):
+//   - less than 16 rows: the weight stream over tiles of 16 rows, waves of eight K
+//     blocks.  64 columns a workgroup in two K groups (256 experts N = 1024 K =
+//     2048: 128 rows 36 us, 5.9 TB/s; 2048 rows 86 us, tiles 94), 32 in four where
+//     the grid is small then (8 rows 7.5 us against 8.3; 64 experts K = 5120 6 rows
+//     12.0 against 15.1), one K group up to K = 512; 256 columns for K <= 256 (64
+//     experts' 1024 rows of N = 512 6.4 us against 7.2);
+//   - few tiles: 64 x 64 (8 experts N = K = 512, 1024 rows 5.2 us, 128 x 256 8);
+//   - up to 47 rows: 64 x 128, three workgroups a CU (256 experts N = 1024 K = 2048,
+//     32 rows 61 us, 128 x 256 69);
+//   - else 128 x 256, two workgroups a CU, so one's stores run under the other's
+//     MFMAs (256 experts N = 1024 K = 2048, 65536 rows 174 us; 256 x 256 190, 128 x
+//     128 229); up to K = 256 128 x 128, three a CU (128 experts N = 512, 65536 rows
+//     27.5 us against 29.8).
 int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const int* offsets, const int* rows,
                            const uint8_t* w, size_t w_stride, const float* wsc, uint16_t* c, int64_t ldc, int S,
                            int Ma, int E, int N, int K, hipStream_t st) {
@@ -802,8 +818,21 @@ int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const
   p.rows = rows;
   p.E = E;
   p.Ma = Ma;
-  if (S / E > 64)
-    return launch_tile<128, 128, 2, 2, 1, 4, 1, 2, true>(
-        p, static_cast<int64_t>(tile_bound(S, E, 128)) * ((N + 127) / 128), st);
-  return launch_tile<64, 64, 2, 2, 1, 4, 1, 4, true>(p, static_cast<int64_t>(tile_bound(S, E, 64)) * ((N + 63) / 64), st);
+  const int avg = S / E;
+  auto wgs = [&](int bm, int bn) { return static_cast<int64_t>(tile_bound(S, E, bm)) * ((N + bn - 1) / bn); };
+  if (avg < 16 && tile_bound(S, E, 16) <= 65535) {
+    auto cut = [&](int tw, int kw, int t, int r) {
+      const int run = kw * r;
+      return StreamCfg{1, tw, kw, t, r, 16, ((N + 15) / 16 + tw * t - 1) / (tw * t), tile_bound(S, E, 16),
+                       1, (p.KS + run - 1) / run};
+    };
+    if (p.KS <= 4) return launch_stream<1, 2, 4, true, true>(cut(8, 1, 2, 4), p, st);
+    if (p.KS <= 8) return launch_stream<1, 1, 8, true, true>(cut(4, 1, 1, 8), p, st);
+    if (p.KS > 16 && wgs(16, 64) <= 512) return launch_stream<1, 1, 8, true, true>(cut(2, 4, 1, 8), p, st);
+    return launch_stream<1, 1, 8, true, true>(cut(4, 2, 1, 8), p, st);
+  }
+  if (wgs(64, 64) <= 512) return launch_tile<64, 64, 2, 2, 1, 4, 2, 2, true>(p, wgs(64, 64), st);
+  if (avg < 48) return launch_tile<64, 128, 1, 4, 1, 4, 1, 3, true>(p, wgs(64, 128), st);
+  if (p.KS <= 4) return launch_tile<128, 128, 2, 2, 1, 3, 1, 3, true>(p, wgs(128, 128), st);
+  return launch_tile<128, 256, 2, 2, 1, 3, 1, 2, true>(p, wgs(128, 256), st);
 }
