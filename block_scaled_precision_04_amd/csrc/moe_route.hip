@@ -1,10 +1,12 @@
 // Routing of tokens to experts: scores, the choice of k experts and their
 // weights, and the gradient of the weights.
 //
-// One wave per token.  Scores, group sums and the order of the choice are held in
-// fp64: ids are discrete, and fp32 scores of different logits meet often enough
-// (about one token in 10^4 has two within an ulp or two at the border of the
-// choice) that their order would differ from the definition's.
+// One wave per token.  ids are discrete, and fp32 scores of different logits meet
+// often enough (about one token in 10^4 has two within an ulp or two at the border
+// of the choice) that their order would differ from the definition's: where the
+// order of scores or of group sums is not clear in fp32, it is decided in fp64.
+#include <algorithm>
+
 #include "common.h"
 
 namespace {
@@ -29,6 +31,13 @@ BS_INLINE float load_logit(const void* p, size_t i) {
   else return static_cast<const float*>(p)[i];
 }
 
+// LDS accesses of one wave run in program order; this keeps the compiler from
+// moving them.
+BS_INLINE void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 BS_INLINE double wave_max_f64(double v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
@@ -38,22 +47,12 @@ BS_INLINE double wave_max_f64(double v) {
   return v;
 }
 
-// Expert e = 64 * i + lane sits in register i of its lane.
+// The choice and the scores of token t in fp64: lane j's pick and its score (-1, 0
+// where there is none).  Expert e = 64 * i + lane sits in register i of its lane;
+// s_val: 64 * V doubles of the wave.
 template <int V, bool BF16, bool SIGMOID>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
-  __shared__ double s_val[kWaves][64 * V];
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-  const int t = blockIdx.x * kWaves + wave;
+BS_INLINE void route_exact(const RouteArgs& p, int t, int l, double* s_val, int& my_id, double& my_s) {
   const double ninf = -__builtin_inf();
-  if (t >= p.T) return;
-  const size_t o = static_cast<size_t>(t) * p.k;
-  if (p.rows != nullptr && t >= *p.rows) {
-    if (l < p.k) {
-      p.ids[o + l] = -1;
-      p.weights[o + l] = 0.0f;
-    }
-    return;
-  }
   double x[V], sc[V], val[V];
   double mx = ninf;
   bool bad = false;
@@ -94,9 +93,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
   if (p.groups > 1) {
     // 64 / G2 lanes to a group (G2: groups rounded up to a power of two)
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_val[wave][64 * i + l] = val[i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    for (int i = 0; i < V; ++i) s_val[64 * i + l] = val[i];
+    wave_lds_fence();
     const int size = p.E / p.groups;
     int part = 64;
     while (part * p.groups > 64) part >>= 1;
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
     double a = ninf, b = ninf;   // the two largest
     if (g < p.groups)
       for (int i = at; i < size; i += part) {
-        const double v = s_val[wave][g * size + i];
+        const double v = s_val[g * size + i];
         if (v > a) {
           b = a;
           a = v;
@@ -133,8 +131,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
       if (!((kept >> (e / size * part)) & 1)) val[i] = ninf;
     }
   }
-  int my_id = -1;
-  double my_s = 0.0;
+  my_id = -1;
+  my_s = 0.0;
   for (int j = 0; j < p.k; ++j) {
     double m = ninf;
 #pragma unroll
@@ -159,6 +157,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
       my_s = s;
     }
   }
+}
+
+// Weights of the picks: lane j's score my_s over the sum of all (renorm), in fp64.
+BS_INLINE void store_picks(const RouteArgs& p, size_t o, int l, int my_id, double my_s) {
   double w = my_s;
   if (p.renorm) {
     const double sum = wave_sum_f64(my_s);
@@ -168,6 +170,285 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p) {
     p.ids[o + l] = my_id;
     p.weights[o + l] = my_id < 0 ? 0.0f : static_cast<float>(w * static_cast<double>(p.scale));
   }
+}
+
+BS_INLINE bool padding(const RouteArgs& p, int t, size_t o, int l) {
+  if (p.rows == nullptr || t < *p.rows) return false;
+  if (l < p.k) {
+    p.ids[o + l] = -1;
+    p.weights[o + l] = 0.0f;
+  }
+  return true;
+}
+
+// Any E and groups, all in fp64.
+template <int V, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_route_f64(RouteArgs p) {
+  __shared__ double s_val[kWaves][64 * V];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int t = blockIdx.x * kWaves + wave;
+  if (t >= p.T) return;
+  const size_t o = static_cast<size_t>(t) * p.k;
+  if (padding(p, t, o, l)) return;
+  int my_id;
+  double my_s;
+  route_exact<V, BF16, SIGMOID>(p, t, l, s_val[wave], my_id, my_s);
+  store_picks(p, o, l, my_id, my_s);
+}
+
+// The largest of the wave's values, in all lanes: within rows of 16 by row shifts,
+// then across the rows (DPP moves, no LDS round trips).
+BS_INLINE float wave_fmax(float v) {
+  constexpr int kNinf = static_cast<int>(0xFF800000u);
+#define BS_STEP(ctrl_, rows_) \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(kNinf, __float_as_int(v), ctrl_, rows_, 0xF, false)))
+  BS_STEP(0x111, 0xF);   // row_shr:1
+  BS_STEP(0x112, 0xF);   // row_shr:2
+  BS_STEP(0x114, 0xF);   // row_shr:4
+  BS_STEP(0x118, 0xF);   // row_shr:8
+  BS_STEP(0x142, 0xA);   // row 0 -> 1, 2 -> 3
+  BS_STEP(0x143, 0xC);   // rows 0-1 -> 2-3
+#undef BS_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+BS_INLINE float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+
+// 2^x of the hardware with the rounding error of the product d * log2(e) added back
+BS_INLINE float exp_near(float d) {
+  const float p = d * 1.44269502f, lo = fmaf(d, 1.44269502f, -p);
+  const float e = __builtin_amdgcn_exp2f(p);
+  return fmaf(e, lo * 0.693147181f, e);
+}
+
+// e^(x - mx) to about an ulp and a half: the rounding error of the difference (which
+// would cost |x - mx| / 2 ulps) and the rest of log2(e) go the same way.
+BS_INLINE float exp_diff(float x, float mx) {
+  const float d = x - mx, b = d - x, err = (x - (d - b)) - (mx + b);
+  const float p = d * 1.44269502f, lo = fmaf(d, 1.44269502f, -p) + fmaf(d, 1.92596299e-8f, err * 1.44269502f);
+  const float e = __builtin_amdgcn_exp2f(p);
+  return fmaf(e, lo * 0.693147181f, e);
+}
+
+// V consecutive logits of a token from expert e0 on (-inf past E).  wide: rows and
+// E are whole vectors of V.
+template <int V, bool BF16>
+BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wide, float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = -__builtin_inff();
+  if (e0 >= E) return;
+  if (wide) {
+    if constexpr (BF16) {
+      const uint16_t* at = static_cast<const uint16_t*>(base) + row + e0;
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int i = 0; i < V; i += 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(at + i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[i + 2 * j] = bf16_lo(w[j]);
+            x[i + 2 * j + 1] = bf16_hi(w[j]);
+          }
+        }
+      } else if constexpr (V == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+      } else if constexpr (V == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
+        x[0] = bf16_lo(w); x[1] = bf16_hi(w);
+      } else {
+        x[0] = bf16_lo(*at);
+      }
+    } else {
+      const float* at = static_cast<const float*>(base) + row + e0;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(at + i);
+          x[i] = w.x; x[i + 1] = w.y; x[i + 2] = w.z; x[i + 3] = w.w;
+        }
+      } else if constexpr (V == 2) {
+        const float2 w = *reinterpret_cast<const float2*>(at);
+        x[0] = w.x; x[1] = w.y;
+      } else {
+        x[0] = *at;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) x[i] = load_logit<BF16>(base, row + e0 + i);
+  }
+}
+
+// The quick form: V consecutive experts a lane, the choice by fp32 values.  Without a
+// bias (and with groups of group_top 1) these are the logits themselves, and the
+// order is exact.  Else they are scores within kTau of the real ones: where two
+// values that the order or the border of the choice hangs on are closer than that
+// (about one token in 500 of 256 sigmoids), and for rows with a NaN or +inf, the
+// wave starts again in fp64.  Weights are fp64 either way, from the picks' logits.
+// A lane keeps its values sorted, in lists of four, so a pick is one reduction over
+// the lanes' heads and one shift in the winner's list (16384 tokens, 8 of 256: with
+// every value compared anew in fp64 38 us).
+// GROUPS: a group is `part` lanes, a power of two.
+constexpr float kTau = 0x1p-19f;
+
+template <int V, bool BF16, bool SIGMOID, bool GROUPS>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wide, int part) {
+  constexpr int LS = V < 4 ? V : 4, NL = V / LS;   // lists of LS values
+  __shared__ double s_val[kWaves][64 * V];         // (the fp64 form's values; here the logits)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int t = blockIdx.x * kWaves + wave;
+  if (t >= p.T) return;
+  const size_t o = static_cast<size_t>(t) * p.k;
+  if (padding(p, t, o, l)) return;
+  const float ninf = -__builtin_inff();
+  const int e0 = l * V;
+  float x[V], v[V];
+  load_logits<V, BF16>(p.logits, static_cast<size_t>(t) * p.ld, e0, p.E, wide, x);
+  float* s_x = reinterpret_cast<float*>(s_val[wave]);
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_x[e0 + i] = x[i];
+
+  const bool by_logit = p.bias == nullptr && (!GROUPS || p.top == 1);
+  float mx = x[0];
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    odd |= !(x[i] < __builtin_inff());
+    mx = fmaxf(mx, x[i]);
+  }
+  bool redo = __ballot(odd) != 0;
+  mx = wave_fmax(mx);
+  double total = 1.0;     // softmax: the sum of exp(x - mx)
+  float largest = 1.0f;   // of the scores
+  const bool scored = !by_logit || (!SIGMOID && !p.renorm);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = x[i];
+  if (scored) {
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // (below -80 the score is 0 to within kTau)
+        const float e = exp_near(fminf(-x[i], 80.0f));
+        v[i] = __builtin_amdgcn_rcpf(1.0f + e);
+      }
+    } else {
+      double part_sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] = exp_near(fmaxf(x[i] - mx, -100.0f));
+        v[i] = x[i] - mx < -100.0f ? 0.0f : v[i];     // (off: -inf)
+        part_sum += static_cast<double>(v[i]);
+      }
+      total = wave_sum_f64(part_sum);
+      largest = 1.0f / static_cast<float>(total);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= largest;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (by_logit) {
+        v[i] = x[i];
+      } else {
+        if (p.bias != nullptr) {
+          const float b = e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
+          v[i] += b;
+          odd |= !(b < __builtin_inff());
+        }
+        v[i] = x[i] == ninf ? ninf : v[i];
+      }
+    }
+    redo |= __ballot(odd) != 0;
+  }
+
+  int my_id = -1;
+  if (!redo) {
+    // each list sorted: value downwards, equal ones in the order of their index
+    // (only neighbours change places)
+    int id[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) id[i] = e0 + i;
+#pragma unroll
+    for (int q = 0; q < NL; ++q)
+#pragma unroll
+      for (int i = 1; i < LS; ++i)
+#pragma unroll
+        for (int j = i; j >= 1; --j) {
+          float &a = v[q * LS + j - 1], &b = v[q * LS + j];
+          int &ia = id[q * LS + j - 1], &ib = id[q * LS + j];
+          const bool up = b > a;
+          const float hi = fmaxf(a, b), lo = fminf(a, b);
+          const int ih = up ? ib : ia, il = up ? ia : ib;
+          a = hi;
+          b = lo;
+          ia = ih;
+          ib = il;
+        }
+    if constexpr (GROUPS) {
+      float a = v[0], b = LS > 1 ? v[LS > 1 ? 1 : 0] : ninf;   // the two largest
+      auto join = [&](float a2, float b2) {
+        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+        a = fmaxf(a, a2);
+      };
+      if constexpr (NL == 2) join(v[4], v[5]);
+      for (int s = 1; s < part; s <<= 1) join(__shfl_xor(a, s, 64), __shfl_xor(b, s, 64));
+      const float u = p.top == 2 ? a + b : a;
+      const int g = l / part;
+      int before = 0;
+      for (int h = 0; h < p.groups; ++h) {
+        const float w = lane_of(u, h * part);
+        before += w > u || (w == u && h < g) ? 1 : 0;
+      }
+      const bool here = g < p.groups;
+      if (p.keep < p.groups && !by_logit) {   // the border
+        const float in = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep - 1)));
+        const float out = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep)));
+        redo = !(in - out > 2.0f * kTau * (2.0f * largest + fabsf(in) + fabsf(out)));
+      }
+      const bool off = !here || before >= p.keep;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = off ? ninf : v[i];
+    }
+    float last = __builtin_inff();
+    const int rounds = by_logit ? p.k : p.k + 1;     // one more to see the border
+    for (int j = 0; j < rounds; ++j) {
+      const bool second = NL == 2 && v[NL == 2 ? 4 : 0] > v[0];
+      const float head = second ? v[NL == 2 ? 4 : 0] : v[0];
+      const float m = wave_fmax(head);
+      if (m == ninf) break;
+      if (!by_logit) redo |= !(last - m > kTau * (largest + fabsf(m)));
+      last = m;
+      if (j == p.k) break;
+      const int w = __builtin_ctzll(__ballot(head == m));
+      const int pick = __builtin_amdgcn_readlane(second ? id[NL == 2 ? 4 : 0] : id[0], w);
+      my_id = l == j ? pick : my_id;
+      if (l == w) {
+#pragma unroll
+        for (int q = 0; q < NL; ++q)
+          if ((q == 1) == second) {
+#pragma unroll
+            for (int i = 0; i + 1 < LS; ++i) {
+              v[q * LS + i] = v[q * LS + i + 1];
+              id[q * LS + i] = id[q * LS + i + 1];
+            }
+            v[q * LS + LS - 1] = ninf;
+          }
+      }
+    }
+  }
+  double my_s;
+  if (redo) {
+    wave_lds_fence();
+    route_exact<V, BF16, SIGMOID>(p, t, l, s_val[wave], my_id, my_s);
+  } else {
+    wave_lds_fence();
+    const double xj = s_x[max(my_id, 0)];
+    const double ref = SIGMOID ? 0.0 : static_cast<double>(mx);
+    const double e = exp(SIGMOID ? -xj : xj - ref);
+    my_s = my_id < 0 ? 0.0 : (SIGMOID ? 1.0 / (1.0 + e) : (p.renorm ? e : e / total));
+  }
+  store_picks(p, o, l, my_id, my_s);
 }
 
 struct RouteBwdArgs {
@@ -181,101 +462,190 @@ struct RouteBwdArgs {
   float scale;
 };
 
-// Lane j holds choice j; the gradients are added up by expert in LDS, in the
-// order of j, and the row is written from there.
-template <int V, bool BF16, bool SIGMOID>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p) {
-  __shared__ double s_d[kWaves][64 * V];
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-  const int t = blockIdx.x * kWaves + wave;
-  const double ninf = -__builtin_inf();
-  if (t >= p.T) return;
-  double* d = s_d[wave];
-  double x[V], mx = ninf, sum = 0.0;
+// V consecutive values of a gradient row.
+template <int V, bool BF16>
+BS_INLINE void store_row(void* base, size_t row, int e0, int E, bool wide, const float (&d)[V]) {
+  if (e0 >= E) return;
+  if constexpr (BF16) {
+    uint32_t w[(V + 1) / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 64 * i + l;
-    x[i] = e < p.E ? load_logit<BF16>(p.logits, static_cast<size_t>(t) * p.ld + e) : -__builtin_inff();
-    mx = x[i] > mx ? x[i] : mx;
-    d[e] = 0.0;
+    for (int i = 0; i < V; i += 2) w[i / 2] = bf16x2_rne(d[i], i + 1 < V ? d[i + 1 < V ? i + 1 : i] : 0.0f);
+    uint16_t* at = static_cast<uint16_t*>(base) + row + e0;
+    if (wide && V > 1) {
+      if constexpr (V == 2) *reinterpret_cast<uint32_t*>(at) = w[0];
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+      if constexpr (V >= 8)
+#pragma unroll
+        for (int i = 0; i < V; i += 8)
+          *reinterpret_cast<uint4*>(at + i) = make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) at[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+  } else {
+    float* at = static_cast<float*>(base) + row + e0;
+    if (wide && V > 1) {
+      if constexpr (V == 2) *reinterpret_cast<float2*>(at) = make_float2(d[0], d[1]);
+      if constexpr (V >= 4)
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(at + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e0 + i < E) at[i] = d[i];
   }
-  mx = wave_max_f64(mx);
-  const size_t o = static_cast<size_t>(t) * p.k;
+}
+
+// The gradient: lane j holds choice j (its part in fp64), lane l experts l * V ..
+// l * V + V - 1 of the row.  The choices' parts go to their experts' places in LDS;
+// where an expert is there twice, one after the other, in the order of j.  Only a
+// softmax over all experts needs the row's logits (DENSE), the others those of the
+// choices.  Bound by the rows' stores and launch (16384 x 256 fp32, 8 choices: 16.8
+// MB written).
+template <int V, bool BF16, bool SIGMOID, bool DENSE>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p, bool wide) {
+  __shared__ __attribute__((aligned(16))) float s_d[kWaves][64 * V];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int t = blockIdx.x * kWaves + wave;
+  if (t >= p.T) return;
+  float* d = s_d[wave];
+  const size_t o = static_cast<size_t>(t) * p.k, row = static_cast<size_t>(t) * p.ld;
+  const int e0 = l * V;
+  float x[V];
+  if constexpr (DENSE) load_logits<V, BF16>(p.logits, row, e0, p.E, wide, x);
   const int id = l < p.k ? p.ids[o + l] : -1;
   const bool there = id >= 0 && id < p.E;
   const double g = there ? p.dw[o + l] : 0.0;
-  const double lx = there ? load_logit<BF16>(p.logits, static_cast<size_t>(t) * p.ld + id) : 0.0;
-  const bool dense = !SIGMOID && !p.renorm;
-  double s;
+  const float lx = there ? load_logit<BF16>(p.logits, row + id) : -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < V; ++i) d[e0 + i] = 0.0f;
+  float near = 0.0f;       // DENSE: 1 / the sum of exp(x - mx)
+  double s, dot = 0.0, mine;
+  const double c = p.scale;
   if constexpr (SIGMOID) {
-    s = there ? 1.0 / (1.0 + exp(-lx)) : 0.0;
+    s = there ? 1.0 / (1.0 + exp(-static_cast<double>(lx))) : 0.0;
   } else {
-    s = !there || lx == ninf ? 0.0 : exp(lx - mx);
-    if (dense) {
+    float mx = lx;
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) mx = fmaxf(mx, x[i]);
+    }
+    mx = wave_fmax(mx);
+    if constexpr (!DENSE) s = lx == -__builtin_inff() ? 0.0 : exp(static_cast<double>(lx) - static_cast<double>(mx));
+    if constexpr (DENSE) {
+      double part = 0.0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        x[i] = x[i] == ninf ? 0.0 : exp(x[i] - mx);
-        sum += x[i];
+        // (a NaN stays one; an expert that is off, and the places past E, give 0)
+        x[i] = x[i] - mx < -100.0f || x[i] == -__builtin_inff() ? 0.0f : exp_diff(x[i], mx);
+        part += static_cast<double>(x[i]);
       }
-      sum = wave_sum_f64(sum);
-      const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
-      s *= inv;
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] *= inv;
+      // the choices' scores from the very values that the sum is made of: g - dot is
+      // then as exact as its terms, where one score is nearly 1 too
+      s = lx - mx < -100.0f || lx == -__builtin_inff() ? 0.0 : static_cast<double>(exp_diff(lx, mx));
+      const double total = wave_sum_f64(part);
+      s = total == 0.0 ? 0.0 : s / total;
+      near = total == 0.0 ? 0.0f : static_cast<float>(1.0 / total);
     }
   }
-  double mine, dot = 0.0;
-  const double c = p.scale;
-  if (p.renorm) {
+  if constexpr (DENSE) {
+    dot = wave_sum_f64(s * g);
+    mine = g;
+  } else if (SIGMOID && !p.renorm) {
+    mine = c * g * s * (1.0 - s);
+  } else {
     const double total = wave_sum_f64(s);
     const double q = total == 0.0 ? 0.0 : s / total;
     dot = wave_sum_f64(q * g);
     mine = c * q * (g - dot);
     if (SIGMOID) mine *= 1.0 - s;
-  } else if (SIGMOID) {
-    mine = c * g * s * (1.0 - s);
+  }
+  const float add = static_cast<float>(mine);
+  // every choice leaves its number at its expert; one that finds another there again
+  // shares the expert
+  int* tag = reinterpret_cast<int*>(d);
+  wave_lds_fence();
+  if (there) tag[id] = l;
+  wave_lds_fence();
+  const bool shared = there && tag[id] != l;
+  wave_lds_fence();
+  if (__ballot(shared) == 0) {
+    if (there) d[id] = add;
   } else {
-    dot = wave_sum_f64(s * g);
-    mine = g;
+    if (there) d[id] = 0.0f;
+    wave_lds_fence();
+    for (int j = 0; j < p.k; ++j) {
+      if (l == j && there) d[id] += add;
+      wave_lds_fence();
+    }
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  for (int j = 0; j < p.k; ++j)
-    if (l == j && there) d[id] += mine;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_fence();
+  float out[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 64 * i + l;
-    if (e >= p.E) break;
-    const double v = dense ? c * x[i] * (d[e] - dot) : d[e];
-    const size_t at = static_cast<size_t>(t) * p.ldd + e;
-    if constexpr (BF16) static_cast<uint16_t*>(p.dl)[at] = static_cast<uint16_t>(bf16x2_rne(static_cast<float>(v), 0.0f));
-    else static_cast<float*>(p.dl)[at] = static_cast<float>(v);
+  for (int i = 0; i < V; ++i) out[i] = d[e0 + i];
+  if constexpr (DENSE) {
+    const float cf = p.scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[i] = cf * (x[i] * near) * static_cast<float>(static_cast<double>(out[i]) - dot);
   }
+  store_row<V, BF16>(p.dl, static_cast<size_t>(t) * p.ldd, e0, p.E, wide, out);
 }
 
 template <int V>
-int launch_route(const RouteArgs& p, bool bf16, bool sigmoid, hipStream_t st) {
+int launch_route_f64(const RouteArgs& p, bool bf16, bool sigmoid, hipStream_t st) {
   const dim3 grid((p.T + kWaves - 1) / kWaves), block(64 * kWaves);
   if (bf16) {
-    if (sigmoid) k_moe_route<V, true, true><<<grid, block, 0, st>>>(p);
-    else k_moe_route<V, true, false><<<grid, block, 0, st>>>(p);
+    if (sigmoid) k_moe_route_f64<V, true, true><<<grid, block, 0, st>>>(p);
+    else k_moe_route_f64<V, true, false><<<grid, block, 0, st>>>(p);
   } else {
-    if (sigmoid) k_moe_route<V, false, true><<<grid, block, 0, st>>>(p);
-    else k_moe_route<V, false, false><<<grid, block, 0, st>>>(p);
+    if (sigmoid) k_moe_route_f64<V, false, true><<<grid, block, 0, st>>>(p);
+    else k_moe_route_f64<V, false, false><<<grid, block, 0, st>>>(p);
   }
   return bs_launch_status();
 }
+template <int V, bool GROUPS>
+int launch_route(const RouteArgs& p, bool bf16, bool sigmoid, bool wide, int part, hipStream_t st) {
+  const dim3 grid((p.T + kWaves - 1) / kWaves), block(64 * kWaves);
+  if (bf16) {
+    if (sigmoid) k_moe_route<V, true, true, GROUPS><<<grid, block, 0, st>>>(p, wide, part);
+    else k_moe_route<V, true, false, GROUPS><<<grid, block, 0, st>>>(p, wide, part);
+  } else {
+    if (sigmoid) k_moe_route<V, false, true, GROUPS><<<grid, block, 0, st>>>(p, wide, part);
+    else k_moe_route<V, false, false, GROUPS><<<grid, block, 0, st>>>(p, wide, part);
+  }
+  return bs_launch_status();
+}
+// The quick form with V values a lane, if the groups fit it; V and BS_OK or an error
+// in status.
+template <int V>
+bool try_route(const RouteArgs& p, bool bf16, bool sigmoid, hipStream_t st, int& status) {
+  if (p.E > 64 * V) return false;
+  const int size = p.E / p.groups, part = size / V, bytes = V * (bf16 ? 2 : 4);
+  const bool wide = p.E % V == 0 && p.ld % V == 0 && bs_aligned(p.logits, std::min(bytes, 16));
+  if (p.groups == 1) {
+    status = launch_route<V, false>(p, bf16, sigmoid, wide, 64, st);
+    return true;
+  }
+  if (size % V || (part & (part - 1)) || part > 64) return false;
+  status = launch_route<V, true>(p, bf16, sigmoid, wide, part, st);
+  return true;
+}
+
 template <int V>
 int launch_route_bwd(const RouteBwdArgs& p, bool bf16, bool sigmoid, hipStream_t st) {
   const dim3 grid((p.T + kWaves - 1) / kWaves), block(64 * kWaves);
+  const uintptr_t bytes = std::min(V * (bf16 ? 2 : 4), 16);
+  const bool wide = p.E % V == 0 && p.ld % V == 0 && p.ldd % V == 0 && bs_aligned(p.logits, bytes) && bs_aligned(p.dl, bytes);
   if (bf16) {
-    if (sigmoid) k_moe_route_bwd<V, true, true><<<grid, block, 0, st>>>(p);
-    else k_moe_route_bwd<V, true, false><<<grid, block, 0, st>>>(p);
+    if (sigmoid) k_moe_route_bwd<V, true, true, false><<<grid, block, 0, st>>>(p, wide);
+    else if (p.renorm) k_moe_route_bwd<V, true, false, false><<<grid, block, 0, st>>>(p, wide);
+    else k_moe_route_bwd<V, true, false, true><<<grid, block, 0, st>>>(p, wide);
   } else {
-    if (sigmoid) k_moe_route_bwd<V, false, true><<<grid, block, 0, st>>>(p);
-    else k_moe_route_bwd<V, false, false><<<grid, block, 0, st>>>(p);
+    if (sigmoid) k_moe_route_bwd<V, false, true, false><<<grid, block, 0, st>>>(p, wide);
+    else if (p.renorm) k_moe_route_bwd<V, false, false, false><<<grid, block, 0, st>>>(p, wide);
+    else k_moe_route_bwd<V, false, false, true><<<grid, block, 0, st>>>(p, wide);
   }
   return bs_launch_status();
 }
@@ -307,12 +677,15 @@ BS_API int moe_route(const void* logits, int64_t ld, int type, const float* bias
   const RouteArgs p{logits, ld, bias, rows, ids, weights, T, E, k, groups, topk_groups, group_top, renorm != 0, scale};
   const bool bf16 = type == BS_TYPE_BF16, sigmoid = score == BS_SCORE_SIGMOID;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int v = (E + 63) / 64;
-  if (v <= 1) return launch_route<1>(p, bf16, sigmoid, st);
-  if (v <= 2) return launch_route<2>(p, bf16, sigmoid, st);
-  if (v <= 4) return launch_route<4>(p, bf16, sigmoid, st);
-  if (v <= 8) return launch_route<8>(p, bf16, sigmoid, st);
-  return launch_route<16>(p, bf16, sigmoid, st);
+  int status = BS_OK;
+  if (try_route<1>(p, bf16, sigmoid, st, status) || try_route<2>(p, bf16, sigmoid, st, status) ||
+      try_route<4>(p, bf16, sigmoid, st, status) || try_route<8>(p, bf16, sigmoid, st, status))
+    return status;
+  const int v = (E + 63) / 64;   // more than 512 experts, or groups that are no whole lanes
+  if (v <= 2) return launch_route_f64<2>(p, bf16, sigmoid, st);
+  if (v <= 4) return launch_route_f64<4>(p, bf16, sigmoid, st);
+  if (v <= 8) return launch_route_f64<8>(p, bf16, sigmoid, st);
+  return launch_route_f64<16>(p, bf16, sigmoid, st);
 }
 
 BS_API int moe_route_backward(const float* dweights, const void* logits, int64_t ld, int type, const int32_t* ids,
