@@ -159,11 +159,73 @@ BS_INLINE void route_exact(const RouteArgs& p, int t, int l, double* s_val, int&
   }
 }
 
+// The largest of the wave's values, in all lanes: within rows of 16 by row shifts,
+// then across the rows (DPP moves, no LDS round trips).
+BS_INLINE float wave_fmax(float v) {
+  constexpr int kNinf = static_cast<int>(0xFF800000u);
+#define BS_STEP(ctrl_, rows_) \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(kNinf, __float_as_int(v), ctrl_, rows_, 0xF, false)))
+  BS_STEP(0x111, 0xF);   // row_shr:1
+  BS_STEP(0x112, 0xF);   // row_shr:2
+  BS_STEP(0x114, 0xF);   // row_shr:4
+  BS_STEP(0x118, 0xF);   // row_shr:8
+  BS_STEP(0x142, 0xA);   // row 0 -> 1, 2 -> 3
+  BS_STEP(0x143, 0xC);   // rows 0-1 -> 2-3
+#undef BS_STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+// fp32 values as unsigned numbers of the same order; 0, below all of them, is "off".
+BS_INLINE uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);   // (-0 is 0)
+  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+BS_INLINE float value_of(uint32_t key) {
+  return __uint_as_float(key ^ (static_cast<int>(key) < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+// The wave's largest key: one instruction a step.
+BS_INLINE uint32_t wave_kmax(uint32_t v) {
+#define BS_STEP(ctrl_, rows_, zero_) \
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), ctrl_, rows_, 0xF, zero_)))
+  BS_STEP(0x111, 0xF, true);
+  BS_STEP(0x112, 0xF, true);
+  BS_STEP(0x114, 0xF, true);
+  BS_STEP(0x118, 0xF, true);
+  BS_STEP(0x142, 0xA, false);
+  BS_STEP(0x143, 0xC, false);
+#undef BS_STEP
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+BS_INLINE double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// The wave's sum, in all lanes, by the same moves.
+BS_INLINE double wave_sum(double v) {
+#define BS_STEP(ctrl_, rows_, zero_)                                                       \
+  {                                                                                        \
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);                                    \
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), ctrl_, rows_, 0xF, zero_);        \
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), ctrl_, rows_, 0xF, zero_);  \
+    v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);                 \
+  }
+  BS_STEP(0x111, 0xF, true);
+  BS_STEP(0x112, 0xF, true);
+  BS_STEP(0x114, 0xF, true);
+  BS_STEP(0x118, 0xF, true);
+  BS_STEP(0x142, 0xA, false);
+  BS_STEP(0x143, 0xC, false);
+#undef BS_STEP
+  return lane_of(v, 63);
+}
+BS_INLINE float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+
 // Weights of the picks: lane j's score my_s over the sum of all (renorm), in fp64.
 BS_INLINE void store_picks(const RouteArgs& p, size_t o, int l, int my_id, double my_s) {
   double w = my_s;
   if (p.renorm) {
-    const double sum = wave_sum_f64(my_s);
+    const double sum = wave_sum(my_s);
     w = sum == 0.0 ? 0.0 : my_s / sum;
   }
   if (l < p.k) {
@@ -195,23 +257,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_f64(RouteArgs p) {
   route_exact<V, BF16, SIGMOID>(p, t, l, s_val[wave], my_id, my_s);
   store_picks(p, o, l, my_id, my_s);
 }
-
-// The largest of the wave's values, in all lanes: within rows of 16 by row shifts,
-// then across the rows (DPP moves, no LDS round trips).
-BS_INLINE float wave_fmax(float v) {
-  constexpr int kNinf = static_cast<int>(0xFF800000u);
-#define BS_STEP(ctrl_, rows_) \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(kNinf, __float_as_int(v), ctrl_, rows_, 0xF, false)))
-  BS_STEP(0x111, 0xF);   // row_shr:1
-  BS_STEP(0x112, 0xF);   // row_shr:2
-  BS_STEP(0x114, 0xF);   // row_shr:4
-  BS_STEP(0x118, 0xF);   // row_shr:8
-  BS_STEP(0x142, 0xA);   // row 0 -> 1, 2 -> 3
-  BS_STEP(0x143, 0xC);   // rows 0-1 -> 2-3
-#undef BS_STEP
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-BS_INLINE float lane_of(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
 
 // 2^x of the hardware with the rounding error of the product d * log2(e) added back
 BS_INLINE float exp_near(float d) {
@@ -283,15 +328,19 @@ BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wid
 
 // The quick form: V consecutive experts a lane, the choice by fp32 values.  Without a
 // bias (and with groups of group_top 1) these are the logits themselves, and the
-// order is exact.  Else they are scores within kTau of the real ones: where two
-// values that the order or the border of the choice hangs on are closer than that
-// (about one token in 500 of 256 sigmoids), and for rows with a NaN or +inf, the
-// wave starts again in fp64.  Weights are fp64 either way, from the picks' logits.
+// order is exact.  Else they are scores within kTau of the real ones; where two
+// values that the order or the border hangs on are closer than that (about one token
+// in 200 of 256 sigmoids), what is close is decided by fp64 values: the groups' sums
+// all anew, or the picks together with up to kMore that follow them, ranked.  (The
+// whole token anew in fp64 is left to rows with a NaN or +inf and to longer runs of
+// close values: the wave takes 8 us, which a launch of 16384 tokens would wait for at
+// its end.)  Weights are fp64 either way, from the picks' logits.
 // A lane keeps its values sorted, in lists of four, so a pick is one reduction over
 // the lanes' heads and one shift in the winner's list (16384 tokens, 8 of 256: with
 // every value compared anew in fp64 38 us).
 // GROUPS: a group is `part` lanes, a power of two.
 constexpr float kTau = 0x1p-19f;
+constexpr int kMore = 8;
 
 template <int V, bool BF16, bool SIGMOID, bool GROUPS>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wide, int part) {
@@ -341,7 +390,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
         v[i] = x[i] - mx < -100.0f ? 0.0f : v[i];     // (off: -inf)
         part_sum += static_cast<double>(v[i]);
       }
-      total = wave_sum_f64(part_sum);
+      total = wave_sum(part_sum);
       largest = 1.0f / static_cast<float>(total);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= largest;
@@ -362,23 +411,40 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
     redo |= __ballot(odd) != 0;
   }
 
+  // fp64 values of logits f, once the sum is known
+  auto exact_total = [&]() {
+    if constexpr (SIGMOID) return 1.0;
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += x[i] == ninf ? 0.0 : exp(static_cast<double>(x[i]) - static_cast<double>(mx));
+    return wave_sum(sum);
+  };
+  auto exact_value = [&](float f, int e, double sum) {
+    const double d = f, b = p.bias != nullptr ? static_cast<double>(p.bias[e]) : 0.0;
+    if constexpr (SIGMOID) return 1.0 / (1.0 + exp(-d)) + b;
+    else return exp(d - static_cast<double>(mx)) / sum + b;
+  };
   int my_id = -1;
   if (!redo) {
-    // each list sorted: value downwards, equal ones in the order of their index
-    // (only neighbours change places)
+    uint32_t key[V];
     int id[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) id[i] = e0 + i;
+    for (int i = 0; i < V; ++i) {
+      key[i] = v[i] == ninf ? 0u : key_of(v[i]);
+      id[i] = e0 + i;
+    }
+    // each list sorted: downwards, equal ones in the order of their index (only
+    // neighbours change places)
 #pragma unroll
     for (int q = 0; q < NL; ++q)
 #pragma unroll
       for (int i = 1; i < LS; ++i)
 #pragma unroll
         for (int j = i; j >= 1; --j) {
-          float &a = v[q * LS + j - 1], &b = v[q * LS + j];
+          uint32_t &a = key[q * LS + j - 1], &b = key[q * LS + j];
           int &ia = id[q * LS + j - 1], &ib = id[q * LS + j];
           const bool up = b > a;
-          const float hi = fmaxf(a, b), lo = fminf(a, b);
+          const uint32_t hi = max(a, b), lo = min(a, b);
           const int ih = up ? ib : ia, il = up ? ia : ib;
           a = hi;
           b = lo;
@@ -386,14 +452,25 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
           ib = il;
         }
     if constexpr (GROUPS) {
-      float a = v[0], b = LS > 1 ? v[LS > 1 ? 1 : 0] : ninf;   // the two largest
-      auto join = [&](float a2, float b2) {
-        b = fmaxf(fmaxf(b, b2), fminf(a, a2));
-        a = fmaxf(a, a2);
+      uint32_t a = key[0], b = LS > 1 ? key[LS > 1 ? 1 : 0] : 0u;   // the two largest
+      auto join = [&](uint32_t a2, uint32_t b2) {
+        b = max(max(b, b2), min(a, a2));
+        a = max(a, a2);
       };
-      if constexpr (NL == 2) join(v[4], v[5]);
-      for (int s = 1; s < part; s <<= 1) join(__shfl_xor(a, s, 64), __shfl_xor(b, s, 64));
-      const float u = p.top == 2 ? a + b : a;
+      if constexpr (NL == 2) join(key[NL == 2 ? 4 : 0], key[NL == 2 ? 5 : 0]);
+#define BS_JOIN(ctrl_)                                                                                     \
+  join(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), ctrl_, 0xF, 0xF, true)),        \
+       static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), ctrl_, 0xF, 0xF, true)))
+      if (part > 1) BS_JOIN(0xB1);    // lane ^ 1
+      if (part > 2) BS_JOIN(0x4E);    // lane ^ 2
+      if (part > 4) BS_JOIN(0x141);   // the other half of 8 (its lanes are equal by now)
+      if (part > 8) BS_JOIN(0x140);   // the other half of 16
+#undef BS_JOIN
+      for (int s = 16; s < part; s <<= 1)
+        join(static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), s, 64)),
+             static_cast<uint32_t>(__shfl_xor(static_cast<int>(b), s, 64)));
+      const float fa = a == 0u ? ninf : value_of(a), fb = b == 0u ? ninf : value_of(b);
+      const float u = p.top == 2 ? fa + fb : fa;
       const int g = l / part;
       int before = 0;
       for (int h = 0; h < p.groups; ++h) {
@@ -404,36 +481,86 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
       if (p.keep < p.groups && !by_logit) {   // the border
         const float in = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep - 1)));
         const float out = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep)));
-        redo = !(in - out > 2.0f * kTau * (2.0f * largest + fabsf(in) + fabsf(out)));
+        if (!(in - out > 2.0f * kTau * (2.0f * largest + fabsf(in) + fabsf(out)))) {
+          const double sum = exact_total();
+          double da = ninf, db = ninf;
+          auto add = [&](double a2, double b2) {
+            const double lo = a2 > da ? da : a2;
+            da = a2 > da ? a2 : da;
+            db = b2 > db ? b2 : db;
+            db = lo > db ? lo : db;
+          };
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (x[i] != ninf) add(exact_value(x[i], e0 + i, sum), ninf);
+          for (int s = 1; s < part; s <<= 1) add(__shfl_xor(da, s, 64), __shfl_xor(db, s, 64));
+          const double du = p.top == 2 ? da + db : da;
+          before = 0;
+          for (int h = 0; h < p.groups; ++h) {
+            const double w = lane_of(du, h * part);
+            before += w > du || (w == du && h < g) ? 1 : 0;
+          }
+        }
       }
       const bool off = !here || before >= p.keep;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = off ? ninf : v[i];
+      for (int i = 0; i < V; ++i) key[i] = off ? 0u : key[i];
     }
-    float last = __builtin_inff();
-    const int rounds = by_logit ? p.k : p.k + 1;     // one more to see the border
-    for (int j = 0; j < rounds; ++j) {
-      const bool second = NL == 2 && v[NL == 2 ? 4 : 0] > v[0];
-      const float head = second ? v[NL == 2 ? 4 : 0] : v[0];
-      const float m = wave_fmax(head);
-      if (m == ninf) break;
-      if (!by_logit) redo |= !(last - m > kTau * (largest + fabsf(m)));
-      last = m;
-      if (j == p.k) break;
+    int my_key = 0, found = 0;
+    // one more pick; false when no expert is left
+    auto pick = [&]() {
+      const bool second = NL == 2 && key[NL == 2 ? 4 : 0] > key[0];
+      const uint32_t head = second ? key[NL == 2 ? 4 : 0] : key[0];
+      const uint32_t m = wave_kmax(head);
+      if (m == 0u) return false;
       const int w = __builtin_ctzll(__ballot(head == m));
-      const int pick = __builtin_amdgcn_readlane(second ? id[NL == 2 ? 4 : 0] : id[0], w);
-      my_id = l == j ? pick : my_id;
+      const int e = __builtin_amdgcn_readlane(second ? id[NL == 2 ? 4 : 0] : id[0], w);
+      my_id = l == found ? e : my_id;
+      my_key = l == found ? static_cast<int>(m) : my_key;
+      ++found;
       if (l == w) {
 #pragma unroll
         for (int q = 0; q < NL; ++q)
           if ((q == 1) == second) {
 #pragma unroll
             for (int i = 0; i + 1 < LS; ++i) {
-              v[q * LS + i] = v[q * LS + i + 1];
+              key[q * LS + i] = key[q * LS + i + 1];
               id[q * LS + i] = id[q * LS + i + 1];
             }
-            v[q * LS + LS - 1] = ninf;
+            key[q * LS + LS - 1] = 0u;
           }
+      }
+      return true;
+    };
+    while (found < p.k && pick()) {
+    }
+    if (!by_logit) {
+      auto best_left = [&]() { return wave_kmax(NL == 2 ? max(key[0], key[NL == 2 ? 4 : 0]) : key[0]); };
+      auto clear = [&](float m, float n) { return m - n > kTau * (largest + fabsf(m)); };
+      // every pick against the next, the last one against the best that is left
+      uint32_t left = best_left();
+      const uint32_t below = l == found - 1 ? left : static_cast<uint32_t>(__shfl_down(my_key, 1, 64));
+      if (__ballot(l < found && below != 0u && !clear(value_of(my_key), value_of(below))) != 0) {
+        const int kept = found;
+        while (found < min(p.k + kMore, 64) && pick()) {
+        }
+        left = best_left();
+        const float last = value_of(static_cast<uint32_t>(__builtin_amdgcn_readlane(my_key, kept - 1)));
+        if (left != 0u && !clear(last, value_of(left))) {
+          redo = true;
+        } else {
+          wave_lds_fence();
+          const double sum = exact_total(), mine = l < found ? exact_value(s_x[max(my_id, 0)], max(my_id, 0), sum) : ninf;
+          int rank = 0;
+          for (int i = 0; i < found; ++i) {
+            const double other = lane_of(mine, i);
+            const int e = __builtin_amdgcn_readlane(my_id, i);
+            rank += other > mine || (other == mine && e < my_id) ? 1 : 0;
+          }
+          rank = l < found ? rank : l;
+          my_id = __builtin_amdgcn_ds_permute(4 * rank, my_id);
+          my_id = l < kept ? my_id : -1;
+        }
       }
     }
   }
@@ -545,20 +672,20 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p, b
       // the choices' scores from the very values that the sum is made of: g - dot is
       // then as exact as its terms, where one score is nearly 1 too
       s = lx - mx < -100.0f || lx == -__builtin_inff() ? 0.0 : static_cast<double>(exp_diff(lx, mx));
-      const double total = wave_sum_f64(part);
+      const double total = wave_sum(part);
       s = total == 0.0 ? 0.0 : s / total;
       near = total == 0.0 ? 0.0f : static_cast<float>(1.0 / total);
     }
   }
   if constexpr (DENSE) {
-    dot = wave_sum_f64(s * g);
+    dot = wave_sum(s * g);
     mine = g;
   } else if (SIGMOID && !p.renorm) {
     mine = c * g * s * (1.0 - s);
   } else {
-    const double total = wave_sum_f64(s);
+    const double total = wave_sum(s);
     const double q = total == 0.0 ? 0.0 : s / total;
-    dot = wave_sum_f64(q * g);
+    dot = wave_sum(q * g);
     mine = c * q * (g - dot);
     if (SIGMOID) mine *= 1.0 - s;
   }
