@@ -210,6 +210,21 @@ def _on_current(fn, *ts):
     return _raw_stream(cur) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
+_bf16, _i8, _i32, _f32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
+
+
+def _stream_of(dev):
+    """The current stream of the current GPU dev."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+# The int8 and routing calls test an accepted tensor in place (each property of a
+# tensor costs 0.05 us, a call of _arg or a turn of _on_current's loop 0.2 to 0.5):
+# what a test does not accept goes to _arg and _on_current, which accept it or say why.
+def _dense(t, dtype, shape):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
 def _rows(rows, cols, dtype, device):
     """A fresh dense [rows, cols] tensor (with its strides given, torch takes 0.35 us less)."""
     return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
@@ -507,14 +522,17 @@ def bsgemm_w4a4_mxfp4_grouped(a, a_scale, offsets, desc, w_pre, rows=None, out=N
 
 
 def _int8_activation(fn, a, a_scale, desc):
-    """Checked (rows, K) of an int8 activation: codes [M, K], scales [M]."""
-    _need(isinstance(a, torch.Tensor) and a.dim() == 2, fn, "a must be a 2-D tensor [M, K]")
+    """Checked (rows, K, row stride) of an int8 activation: codes [M, K], scales [M]."""
+    if not (isinstance(a, torch.Tensor) and a.dim() == 2):
+        _need(False, fn, "a must be a 2-D tensor [M, K]")
     M, K = a.shape
     if desc.K != K:
         _need(False, fn, f"a has K = {K}, the weight descriptor K = {desc.K}")
-    _arg(fn, "a", a, (M, K), _I8, one_row=True)
-    _arg(fn, "a_scale", a_scale, (M,), _F32, contiguous=True)
-    return M, K
+    if not (a.dtype is _i8 and a.is_contiguous()):
+        _arg(fn, "a", a, (M, K), _I8, one_row=True)
+    if not _dense(a_scale, _f32, (M,)):
+        _arg(fn, "a_scale", a_scale, (M,), _F32, contiguous=True)
+    return M, K, a.stride(0) if M > 1 else K
 
 
 def bsgemm_w8a8_int8(a, a_scale, desc, w_pre, w_scale, out=None, ws=None):
@@ -522,23 +540,32 @@ def bsgemm_w8a8_int8(a, a_scale, desc, w_pre, w_scale, out=None, ws=None):
     multiple of 16); a_scale: fp32 [M]; desc, w_pre: from prelayout_int8;
     w_scale: fp32 [N]; ws: alloc_workspace(BS_OP_W8A8_INT8, M, N, K)."""
     fn = "bsgemm_w8a8_int8"
-    M, K = _int8_activation(fn, a, a_scale, desc)
+    M, K, lda = _int8_activation(fn, a, a_scale, desc)
     N = desc.N
-    _need(isinstance(w_pre, torch.Tensor), fn, "w_pre must be a torch.Tensor")
-    nw = w_pre.numel()
-    _arg(fn, "w_pre", w_pre, (nw,), _U8, contiguous=True)
-    if nw < desc.total_bytes:
-        _need(False, fn, f"w_pre holds {nw} bytes, the layout needs {desc.total_bytes}")
-    _arg(fn, "w_scale", w_scale, (N,), _F32, contiguous=True)
-    if out is None:
-        out = _rows(M, N, torch.bfloat16, a.device)
-    else:
+    if not (isinstance(w_pre, torch.Tensor) and w_pre.dtype is torch.uint8 and w_pre.dim() == 1 and w_pre.is_contiguous()):
+        _need(isinstance(w_pre, torch.Tensor), fn, "w_pre must be a torch.Tensor")
+        _arg(fn, "w_pre", w_pre, (w_pre.numel(),), _U8, contiguous=True)
+    if w_pre.numel() < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {w_pre.numel()} bytes, the layout needs {desc.total_bytes}")
+    if not _dense(w_scale, _f32, (N,)):
+        _arg(fn, "w_scale", w_scale, (N,), _F32, contiguous=True)
+    if out is not None:
         _arg(fn, "out", out, (M, N), _BF16, one_row=True)
-    stream = _on_current(fn, a, a_scale, w_pre, w_scale, out, ws)
+    dev = a.get_device()
+    if dev < 0 or dev != _current_device() or a_scale.get_device() != dev or w_pre.get_device() != dev \
+            or w_scale.get_device() != dev or out is not None or ws is not None:
+        _on_current(fn, a, a_scale, w_pre, w_scale, out, ws)
+    if out is None:
+        out = torch.empty_strided((M, N), (N, 1), dtype=_bf16, device=a.device)
+        ldc = N
+    else:
+        ldc = _row_stride(out)
     ws_p, ws_n = _ws(fn, ws)
-    _check(fn, lib().bsgemm_w8a8_int8(
-        a.data_ptr(), _row_stride(a), a_scale.data_ptr(), ctypes.byref(desc), w_pre.data_ptr(), w_scale.data_ptr(),
-        out.data_ptr(), _row_stride(out), M, N, K, ws_p, ws_n, stream))
+    status = lib().bsgemm_w8a8_int8(
+        a.data_ptr(), lda, a_scale.data_ptr(), ctypes.byref(desc), w_pre.data_ptr(), w_scale.data_ptr(),
+        out.data_ptr(), ldc, M, N, K, ws_p, ws_n, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return out
 
 
@@ -549,28 +576,35 @@ def bsgemm_w8a8_int8_grouped(a, a_scale, offsets, desc, w_pre, w_scale, rows=Non
     w_pre: from prelayout_int8_experts; w_scale: fp32 [E, N].  Rows of out past
     offsets[E] keep what they hold (pass out to choose; a fresh one is not cleared)."""
     fn = "bsgemm_w8a8_int8_grouped"
-    Ma, K = _int8_activation(fn, a, a_scale, desc)
+    Ma, K, lda = _int8_activation(fn, a, a_scale, desc)
     N = desc.N
-    _need(isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
-    E = w_pre.shape[0]
-    _arg(fn, "w_pre", w_pre, (E, w_pre.shape[1]), _U8, one_row=True)
-    if w_pre.shape[1] < desc.total_bytes:
-        _need(False, fn, f"w_pre holds {w_pre.shape[1]} bytes an expert, the layout needs {desc.total_bytes}")
-    _arg(fn, "w_scale", w_scale, (E, N), _F32, contiguous=True)
-    _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
+    if not (isinstance(w_pre, torch.Tensor) and w_pre.dim() == 2):
+        _need(False, fn, "w_pre must be a 2-D tensor [E, total_bytes]")
+    E, nw = w_pre.shape
+    if not (w_pre.dtype is torch.uint8 and w_pre.is_contiguous()):
+        _arg(fn, "w_pre", w_pre, (E, nw), _U8, one_row=True)
+    if nw < desc.total_bytes:
+        _need(False, fn, f"w_pre holds {nw} bytes an expert, the layout needs {desc.total_bytes}")
+    if not _dense(w_scale, _f32, (E, N)):
+        _arg(fn, "w_scale", w_scale, (E, N), _F32, contiguous=True)
+    if not _dense(offsets, _i32, (E + 1,)):
+        _arg(fn, "offsets", offsets, (E + 1,), _I32, contiguous=True)
     S = Ma
     if rows is not None:
         _need(isinstance(rows, torch.Tensor), fn, "rows must be a torch.Tensor")
         S = rows.numel()
-        _arg(fn, "rows", rows, (S,), _I32, contiguous=True)
+        if not _dense(rows, _i32, (S,)):
+            _arg(fn, "rows", rows, (S,), _I32, contiguous=True)
     if out is None:
-        out = _rows(S, N, torch.bfloat16, a.device)
+        out = _rows(S, N, _bf16, a.device)
     else:
         _arg(fn, "out", out, (S, N), _BF16, one_row=True)
     stream = _on_current(fn, a, a_scale, offsets, w_pre, w_scale, rows, out)
-    _check(fn, lib().bsgemm_w8a8_int8_grouped(
-        a.data_ptr(), _row_stride(a), a_scale.data_ptr(), Ma, offsets.data_ptr(), _ptr(rows), ctypes.byref(desc),
-        w_pre.data_ptr(), _row_stride(w_pre), w_scale.data_ptr(), out.data_ptr(), _row_stride(out), S, E, N, K, stream))
+    status = lib().bsgemm_w8a8_int8_grouped(
+        a.data_ptr(), lda, a_scale.data_ptr(), Ma, offsets.data_ptr(), _ptr(rows), ctypes.byref(desc),
+        w_pre.data_ptr(), _row_stride(w_pre), w_scale.data_ptr(), out.data_ptr(), _row_stride(out), S, E, N, K, stream)
+    if status:
+        _check(fn, status)
     return out
 
 
@@ -797,33 +831,48 @@ def dequant_mxfp4(q, scale, out=None):
 
 
 # ------------------------------------------------------------------ int8 quantizers
-def _int8_out(fn, q, scale, M, K, device):
+def _int8_out(fn, q, scale, M, K, like):
+    """(q, scale) as given and checked, or fresh ones on the device of `like`."""
+    dev = like.get_device()
     if q is None:
-        q = _rows(M, K, torch.int8, device)
-    else:
+        q = torch.empty_strided((M, K), (K, 1), dtype=_i8, device=like.device)
+    elif not (_dense(q, _i8, (M, K)) and q.get_device() == dev):
         _arg(fn, "q", q, (M, K), _I8, contiguous=True)
+        _on_device(fn, like, q)
     if scale is None:
-        scale = torch.empty_strided((M,), (1,), dtype=torch.float32, device=device)
-    else:
+        scale = torch.empty_strided((M,), (1,), dtype=_f32, device=like.device)
+    elif not (_dense(scale, _f32, (M,)) and scale.get_device() == dev):
         _arg(fn, "scale", scale, (M,), _F32, contiguous=True)
+        _on_device(fn, like, scale)
     return q, scale
+
+
+def _matrix(fn, name, x, what):
+    """Checked shape of a 2-D bf16 tensor with any strides."""
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+        _need(False, fn, f"{name} must be a 2-D tensor {what}")
+    if x.dtype is not _bf16:
+        _arg(fn, name, x, x.shape, _BF16, unit_inner=False)
+    return x.shape
 
 
 def quant_int8_per_token(x, q=None, scale=None):
     """x bf16 [M, K] (row stride may be padded to a multiple of 8) -> (q int8 [M, K],
     scale fp32 [M]); on a weight [N, K] the codes for prelayout_int8 and w_scale."""
     fn = "quant_int8_per_token"
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, fn, "x must be a 2-D tensor [M, K]")
-    M, K = x.shape
-    _arg(fn, "x", x, (M, K), _BF16, unit_inner=False)
-    q, scale = _int8_out(fn, q, scale, M, K, x.device)
-    stream = _on_current(fn, x, q, scale)
+    M, K = _matrix(fn, "x", x, "[M, K]")
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        _on_current(fn, x)
+    q, scale = _int8_out(fn, q, scale, M, K, x)
     ldx, inner = x.stride()
     if M == 1:
         ldx = K
     if inner != 1 or ldx < K or ldx % 8 or x.data_ptr() % 16:
         x, ldx = x.clone(memory_format=torch.contiguous_format), K
-    _check(fn, lib().quant_int8_per_token(x.data_ptr(), ldx, q.data_ptr(), scale.data_ptr(), M, K, stream))
+    status = lib().quant_int8_per_token(x.data_ptr(), ldx, q.data_ptr(), scale.data_ptr(), M, K, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return q, scale
 
 
@@ -832,23 +881,27 @@ def add_rms_quant_int8(y, residual, gamma, eps=1e-6, offset=1.0, q=None, scale=N
     y + residual with the weight offset + gamma.  residual None: the norm of y
     (residual_out then comes back as it was given)."""
     fn = "add_rms_quant_int8"
-    _need(isinstance(y, torch.Tensor) and y.dim() == 2, fn, "y must be a 2-D tensor [M, K]")
-    M, K = y.shape
-    _arg(fn, "y", y, (M, K), _BF16, unit_inner=False)
-    _arg(fn, "gamma", gamma, (K,), _BF16, unit_inner=False)
-    if residual is not None:
+    shape = M, K = _matrix(fn, "y", y, "[M, K]")
+    if not _dense(gamma, _bf16, (K,)):
+        _arg(fn, "gamma", gamma, (K,), _BF16, unit_inner=False)
+    if residual is not None and not _dense(residual, _bf16, shape):
         _arg(fn, "residual", residual, (M, K), _BF16, unit_inner=False)
-        if residual_out is None:
-            residual_out = _rows(M, K, torch.bfloat16, y.device)
     if residual_out is not None:
         _arg(fn, "residual_out", residual_out, (M, K), _BF16, contiguous=True)
-    q, scale = _int8_out(fn, q, scale, M, K, y.device)
-    stream = _on_current(fn, y, residual, gamma, q, scale, residual_out)
+    dev = y.get_device()
+    if dev < 0 or dev != _current_device() or gamma.get_device() != dev or residual_out is not None \
+            or (residual is not None and residual.get_device() != dev):
+        _on_current(fn, y, residual, gamma, residual_out)
+    q, scale = _int8_out(fn, q, scale, M, K, y)
     y, gamma = _aligned(y), _aligned(gamma)
     if residual is not None:
         residual = _aligned(residual)
-    _check(fn, lib().add_rms_quant_int8(y.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, offset, q.data_ptr(),
-                                        scale.data_ptr(), _ptr(residual_out), M, K, stream))
+        if residual_out is None:
+            residual_out = torch.empty_strided((M, K), (K, 1), dtype=_bf16, device=y.device)
+    status = lib().add_rms_quant_int8(y.data_ptr(), _ptr(residual), gamma.data_ptr(), eps, offset, q.data_ptr(),
+                                      scale.data_ptr(), _ptr(residual_out), M, K, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return q, scale, residual_out
 
 
@@ -857,33 +910,44 @@ def silu_mul_quant_int8(gu, q=None, scale=None, rows=None):
     silu(gate) * up.  rows: optional int32 tensor of one element; only the first
     min(rows, M) rows are computed (e.g. offsets[E:])."""
     fn = "silu_mul_quant_int8"
-    _need(isinstance(gu, torch.Tensor) and gu.dim() == 2 and gu.shape[1] % 2 == 0, fn,
-          "gu must be a 2-D tensor [M, 2N]")
-    M, N = gu.shape[0], gu.shape[1] // 2
-    _arg(fn, "gu", gu, (M, 2 * N), _BF16, unit_inner=False)
+    M, N2 = _matrix(fn, "gu", gu, "[M, 2N]")
+    if N2 % 2:
+        _need(False, fn, "gu must be a 2-D tensor [M, 2N]")
+    N = N2 // 2
     if rows is not None:
         _arg(fn, "rows", rows, (1,), _I32)
-    q, scale = _int8_out(fn, q, scale, M, N, gu.device)
-    stream = _on_current(fn, gu, q, scale, rows)
+    dev = gu.get_device()
+    if dev < 0 or dev != _current_device() or rows is not None:
+        _on_current(fn, gu, rows)
+    q, scale = _int8_out(fn, q, scale, M, N, gu)
     gu = _aligned(gu)
-    _check(fn, lib().silu_mul_quant_int8(gu.data_ptr(), q.data_ptr(), scale.data_ptr(), _ptr(rows), M, N, stream))
+    status = lib().silu_mul_quant_int8(gu.data_ptr(), q.data_ptr(), scale.data_ptr(), _ptr(rows), M, N, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return q, scale
 
 
 def dequant_int8(q, scale, out=None):
     """(q int8 [M, K], scale fp32 [M]) -> the values, bf16 [M, K]."""
     fn = "dequant_int8"
-    _need(isinstance(q, torch.Tensor) and q.dim() == 2, fn, "q must be a 2-D tensor [M, K]")
+    if not (isinstance(q, torch.Tensor) and q.dim() == 2):
+        _need(False, fn, "q must be a 2-D tensor [M, K]")
     M, K = q.shape
-    _arg(fn, "q", q, (M, K), _I8, unit_inner=False)
-    _arg(fn, "scale", scale, (M,), _F32, contiguous=True)
-    if out is None:
-        out = _rows(M, K, torch.bfloat16, q.device)
-    else:
+    if q.dtype is not _i8:
+        _arg(fn, "q", q, (M, K), _I8, unit_inner=False)
+    if not _dense(scale, _f32, (M,)):
+        _arg(fn, "scale", scale, (M,), _F32, contiguous=True)
+    dev = q.get_device()
+    if out is not None:
         _arg(fn, "out", out, (M, K), _BF16, contiguous=True)
-    stream = _on_current(fn, q, scale, out)
+    if dev < 0 or dev != _current_device() or scale.get_device() != dev or out is not None:
+        _on_current(fn, q, scale, out)
+    if out is None:
+        out = torch.empty_strided((M, K), (K, 1), dtype=_bf16, device=q.device)
     q = _aligned(q)
-    _check(fn, lib().dequant_int8(q.data_ptr(), scale.data_ptr(), out.data_ptr(), M, K, stream))
+    status = lib().dequant_int8(q.data_ptr(), scale.data_ptr(), out.data_ptr(), M, K, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return out
 
 
@@ -891,10 +955,16 @@ def dequant_int8(q, scale, out=None):
 _LOGITS = {torch.float32: BS_TYPE_F32, torch.bfloat16: BS_TYPE_BF16}
 
 
-def _moe_logits(fn, name, x, shape):
-    """Checked (type, row stride) of logits [T, E]."""
-    _arg(fn, name, x, shape, tuple(_LOGITS), one_row=True)
-    return _LOGITS[x.dtype], _row_stride(x)
+def _moe_logits(fn, name, x):
+    """Checked (T, E, type, row stride) of logits [T, E]."""
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+        _need(False, fn, f"{name} must be a 2-D tensor [T, E]")
+    T, E = x.shape
+    type_ = _LOGITS.get(x.dtype)
+    if type_ is None or not x.is_contiguous():
+        _arg(fn, name, x, (T, E), tuple(_LOGITS), one_row=True)
+        return T, E, type_, _row_stride(x)
+    return T, E, type_, E
 
 
 def moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, groups=1, topk_groups=1, group_top=1, renorm=True,
@@ -908,27 +978,32 @@ def moe_route(logits, k, bias=None, score=BS_SCORE_SOFTMAX, groups=1, topk_group
     optional int32 tensor of one element, tokens from it on are padding.
     ids and weights go to moe_sort and moe_combine."""
     fn = "moe_route"
-    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2, fn, "logits must be a 2-D tensor [T, E]")
-    T, E = logits.shape
-    type_, ld = _moe_logits(fn, "logits", logits, (T, E))
-    for name, v in (("k", k), ("groups", groups), ("topk_groups", topk_groups), ("group_top", group_top)):
-        if not (isinstance(v, int) and v >= 1):
-            _need(False, fn, f"{name} = {v!r} must be a positive int")
-    if bias is not None:
+    T, E, type_, ld = _moe_logits(fn, "logits", logits)
+    if not (type(k) is int and type(groups) is int and type(topk_groups) is int and type(group_top) is int
+            and k >= 1 and groups >= 1 and topk_groups >= 1 and group_top >= 1):
+        for name, v in (("k", k), ("groups", groups), ("topk_groups", topk_groups), ("group_top", group_top)):
+            _need(isinstance(v, int) and v >= 1, fn, f"{name} = {v!r} must be a positive int")
+    dev = logits.get_device()
+    if bias is not None and not _dense(bias, _f32, (E,)):
         _arg(fn, "bias", bias, (E,), _F32, contiguous=True)
     if rows is not None:
         _arg(fn, "rows", rows, (1,), _I32)
-    if ids is None:
-        ids = _rows(T, k, torch.int32, logits.device)
-    else:
+    if ids is not None:
         _arg(fn, "ids", ids, (T, k), _I32, contiguous=True)
-    if weights is None:
-        weights = _rows(T, k, torch.float32, logits.device)
-    else:
+    if weights is not None:
         _arg(fn, "weights", weights, (T, k), _F32, contiguous=True)
-    stream = _on_current(fn, logits, bias, rows, ids, weights)
-    _check(fn, lib().moe_route(logits.data_ptr(), ld, type_, _ptr(bias), score, groups, topk_groups, group_top,
-                               bool(renorm), scale, _ptr(rows), ids.data_ptr(), weights.data_ptr(), T, E, k, stream))
+    if dev < 0 or dev != _current_device() or bias is not None or rows is not None or ids is not None \
+            or weights is not None:
+        _on_current(fn, logits, bias, rows, ids, weights)
+    if ids is None:
+        ids = torch.empty_strided((T, k), (k, 1), dtype=_i32, device=logits.device)
+    if weights is None:
+        weights = torch.empty_strided((T, k), (k, 1), dtype=_f32, device=logits.device)
+    status = lib().moe_route(logits.data_ptr(), ld, type_, _ptr(bias), score, groups, topk_groups, group_top,
+                             1 if renorm else 0, scale, _ptr(rows), ids.data_ptr(), weights.data_ptr(), T, E, k,
+                             _stream_of(dev))
+    if status:
+        _check(fn, status)
     return ids, weights
 
 
@@ -936,20 +1011,29 @@ def moe_route_backward(dweights, logits, ids, score=BS_SCORE_SOFTMAX, renorm=Tru
     """Gradient of moe_route's weights: dlogits [T, E] of the logits' type, every
     value written.  ids from moe_route; score, renorm, scale as there."""
     fn = "moe_route_backward"
-    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2, fn, "logits must be a 2-D tensor [T, E]")
-    T, E = logits.shape
-    type_, ld = _moe_logits(fn, "logits", logits, (T, E))
-    _need(isinstance(ids, torch.Tensor) and ids.dim() == 2, fn, "ids must be a 2-D tensor [T, k]")
+    T, E, type_, ld = _moe_logits(fn, "logits", logits)
+    if not (isinstance(ids, torch.Tensor) and ids.dim() == 2):
+        _need(False, fn, "ids must be a 2-D tensor [T, k]")
     k = ids.shape[1]
-    _arg(fn, "ids", ids, (T, k), _I32, contiguous=True)
-    _arg(fn, "dweights", dweights, (T, k), _F32, contiguous=True)
+    if not _dense(ids, _i32, (T, k)):
+        _arg(fn, "ids", ids, (T, k), _I32, contiguous=True)
+    if not _dense(dweights, _f32, (T, k)):
+        _arg(fn, "dweights", dweights, (T, k), _F32, contiguous=True)
+    ldd = E
+    if dlogits is not None:
+        _, _, ltype, ldd = _moe_logits(fn, "dlogits", dlogits)
+        _need(ltype == type_, fn, f"dlogits has dtype {dlogits.dtype}, the logits {logits.dtype}")
+        _need(dlogits.shape == logits.shape, fn, f"dlogits has shape {tuple(dlogits.shape)}, expected {(T, E)}")
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device() or ids.get_device() != dev or dweights.get_device() != dev \
+            or dlogits is not None:
+        _on_current(fn, dweights, logits, ids, dlogits)
     if dlogits is None:
-        dlogits = _rows(T, E, logits.dtype, logits.device)
-    _need(dlogits.dtype == logits.dtype, fn, f"dlogits has dtype {dlogits.dtype}, the logits {logits.dtype}")
-    _, ldd = _moe_logits(fn, "dlogits", dlogits, (T, E))
-    stream = _on_current(fn, dweights, logits, ids, dlogits)
-    _check(fn, lib().moe_route_backward(dweights.data_ptr(), logits.data_ptr(), ld, type_, ids.data_ptr(), score,
-                                        bool(renorm), scale, dlogits.data_ptr(), ldd, T, E, k, stream))
+        dlogits = torch.empty_strided((T, E), (E, 1), dtype=logits.dtype, device=logits.device)
+    status = lib().moe_route_backward(dweights.data_ptr(), logits.data_ptr(), ld, type_, ids.data_ptr(), score,
+                                      1 if renorm else 0, scale, dlogits.data_ptr(), ldd, T, E, k, _stream_of(dev))
+    if status:
+        _check(fn, status)
     return dlogits
 
 
