@@ -83,6 +83,12 @@ __global__ __launch_bounds__(1024) void k_w8a8_stream(W8A8Args p) {
     nrows = RS;
   }
 
+  // grouped: byte offset of the row that this lane loads of each row block (looked
+  // up once, not anew for every load of the loop below)
+  static_assert(!GROUPED || MB == 1, "16 rows a workgroup");
+  uint32_t row_off = 0;
+  if constexpr (GROUPED) row_off = static_cast<uint32_t>(src_row(p, m0 + min(l >> 2, nrows - 1))) * p.lda;
+
   // the owner's scales: its row of each row block, its four columns of each tile
   const bool owner = kw == 0;
   float sa[MB], sw[T][4];
@@ -121,16 +127,23 @@ __global__ __launch_bounds__(1024) void k_w8a8_stream(W8A8Args p) {
     // chunk c of row i of block r sits at position (r*RS + i)*4 + swz4(i, c);
     // positions past the slice, and chunks past K, re-read valid bytes (the
     // weight is zero there)
-    for (int k = wave; k < a_instr; k += TW * KW) {
-      const int q = k * 64 + l;
-      const int ri = q >> 2;
-      const int r = min(ri / RS, wg_steps - 1);
-      const int ii = ri % RS;
-      int row = m0 + min(ii, nrows - 1);
-      if constexpr (GROUPED) row = src_row(p, row);
-      dma16(lds0 + k * 1024, p.a,
-            static_cast<uint32_t>(row) * p.lda +
-                static_cast<uint32_t>(min((wg_k0 + r) * 4 + swz4(ii, q & 3), last_chunk) * 16));
+    if constexpr (GROUPED) {   // (RS = 16: a load is 16 rows of a block, the lane's row always the same)
+      for (int k = wave; k < a_instr; k += TW * KW) {
+        const int r = min(k, wg_steps - 1);
+        dma16(lds0 + k * 1024, p.a,
+              row_off + static_cast<uint32_t>(min((wg_k0 + r) * 4 + swz4(l >> 2, l & 3), last_chunk) * 16));
+      }
+    } else {
+      for (int k = wave; k < a_instr; k += TW * KW) {
+        const int q = k * 64 + l;
+        const int ri = q >> 2;
+        const int r = min(ri / RS, wg_steps - 1);
+        const int ii = ri % RS;
+        const int row = m0 + min(ii, nrows - 1);
+        dma16(lds0 + k * 1024, p.a,
+              static_cast<uint32_t>(row) * p.lda +
+                  static_cast<uint32_t>(min((wg_k0 + r) * 4 + swz4(ii, q & 3), last_chunk) * 16));
+      }
     }
     v4i wf[T][R];
 #pragma unroll
@@ -161,6 +174,19 @@ __global__ __launch_bounds__(1024) void k_w8a8_stream(W8A8Args p) {
         for (int mb = 0; mb < MB; ++mb)
           acc[t][mb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[t][r], af[mb], acc[t][mb], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    // All of a turn's weights are waited for here; without this the compiler waits for
+    // the next turn's activation loads before it issues that turn's weight loads.  With
+    // row_off: 16 experts of 4096x4096, 4 tokens, 20.0 -> 18.7 us; 128 of 512x256 5.7 ->
+    // 5.5; 256 of 1024x2048, 32 tokens, 53.9 -> 54.8.  Not for the dense forms: 32 rows
+    // +-2%, and 64 rows, whose activation loads are 4 times as many, are better off with
+    // those ahead of every wave's weights (N = K = 5120 13.8 -> 15.1 us, K = 17408 28.8
+    // -> 33.5).
+    if constexpr (GROUPED) {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r) keep_vgprs(wf[t][r]);
     }
   }
 
