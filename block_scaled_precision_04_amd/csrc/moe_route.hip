@@ -481,7 +481,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
       if (p.keep < p.groups && !by_logit) {   // the border
         const float in = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep - 1)));
         const float out = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep)));
-        if (!(in - out > 2.0f * kTau * (2.0f * largest + fabsf(in) + fabsf(out)))) {
+        // (a sum is off by what its terms are, and those of any group may be large ones
+        // that cancel)
+        const float terms = p.top == 2 ? fabsf(fa) + fabsf(fb) : fabsf(fa);
+        const float most = wave_fmax(terms < __builtin_inff() ? terms : 0.0f);
+        if (!(in - out > 4.0f * kTau * (largest + most))) {
           const double sum = exact_total();
           double da = ninf, db = ninf;
           auto add = [&](double a2, double b2) {
@@ -539,7 +543,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
       auto clear = [&](float m, float n) { return m - n > kTau * (largest + fabsf(m)); };
       // every pick against the next, the last one against the best that is left
       uint32_t left = best_left();
-      const uint32_t below = l == found - 1 ? left : static_cast<uint32_t>(__shfl_down(my_key, 1, 64));
+      const uint32_t next = static_cast<uint32_t>(__shfl_down(my_key, 1, 64));   // (by all lanes: none reads from one that is off)
+      const uint32_t below = l == found - 1 ? left : next;
       if (__ballot(l < found && below != 0u && !clear(value_of(my_key), value_of(below))) != 0) {
         const int kept = found;
         while (found < min(p.k + kMore, 64) && pick()) {

@@ -130,6 +130,44 @@ def test_bias_that_switches_off():
     _close(w, wo)
 
 
+@pytest.mark.parametrize("k,keep", [(8, 4), (1, 1), (2, 2)])
+@pytest.mark.parametrize("big", [100.0, 1000.0, 1e6])
+def test_group_sums_of_large_biases_that_cancel(big, k, keep):
+    """Of each group one expert has +big and the others -big: fp32 sums of the two
+    largest lose the scores that decide between the groups."""
+    T, E, groups = 200, 256, 8
+    x = torch.randn((T, E), generator=torch.Generator().manual_seed(5)).cuda()
+    b = np.full(E, -big)
+    b[np.arange(groups) * 32 + np.arange(groups)] = big
+    bias = torch.from_numpy(b.astype(np.float32)).cuda()
+    ids, w = bs.moe_route(x, k, bias=bias, score=bs.BS_SCORE_SIGMOID, groups=groups, topk_groups=keep, group_top=2)
+    want, ww = route.route(x.double().cpu().numpy(), k, bias.double().cpu().numpy(), True, groups, keep, 2)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    _close(w, ww)
+
+
+@pytest.mark.parametrize("k", [2, 3, 8, 12])
+@pytest.mark.parametrize("bias", [0.0, 1000.0])
+def test_the_last_two_picks_closer_than_fp32(k, bias):
+    """The k-th value just below the (k-1)-th and, by its index, before it where fp32
+    holds them equal; all others far away."""
+    T, E = 64, 64
+    g = np.random.default_rng(k)
+    x = np.full((T, E), -4.0, np.float32)
+    for t in range(T):
+        at = np.sort(g.permutation(E)[:k])
+        x[t, at] = 1.0 + 0.25 * np.arange(k)
+        lo, hi = at[0], at[1]
+        v = np.float32(-1.0 + 0.01 * t)
+        x[t, lo], x[t, hi] = v, v + np.float32(2.0 ** -21 if bias == 0.0 else 1e-5)
+    b = np.full(E, bias, np.float32)
+    dx = torch.from_numpy(x).cuda()
+    ids, w = bs.moe_route(dx, k, bias=torch.from_numpy(b).cuda(), score=bs.BS_SCORE_SIGMOID)
+    want, ww = route.route(x.astype(np.float64), k, b.astype(np.float64), True)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    _close(w, ww)
+
+
 @pytest.mark.parametrize("live", [0, 1, 5, 9, 20, -1])
 def test_padding_tokens(live):
     x, xo = _logits(5, 9, 64, "bf16")
