@@ -320,9 +320,12 @@ BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wid
       }
     }
   } else {
+    // (all loads at once, those past E of the last value)
+    float y[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e0 + i < E) x[i] = load_logit<BF16>(base, row + e0 + i);
+    for (int i = 0; i < V; ++i) y[i] = load_logit<BF16>(base, row + min(e0 + i, E - 1));
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? y[i] : x[i];
   }
 }
 
@@ -342,20 +345,16 @@ BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wid
 constexpr float kTau = 0x1p-19f;
 constexpr int kMore = 8;
 
+// s_val: 64 * V doubles of the wave (the fp64 form's values; here the logits).
 template <int V, bool BF16, bool SIGMOID, bool GROUPS>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wide, int part) {
+BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part, double* s_val) {
   constexpr int LS = V < 4 ? V : 4, NL = V / LS;   // lists of LS values
-  __shared__ double s_val[kWaves][64 * V];         // (the fp64 form's values; here the logits)
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
-  const int t = blockIdx.x * kWaves + wave;
-  if (t >= p.T) return;
   const size_t o = static_cast<size_t>(t) * p.k;
-  if (padding(p, t, o, l)) return;
   const float ninf = -__builtin_inff();
   const int e0 = l * V;
   float x[V], v[V];
   load_logits<V, BF16>(p.logits, static_cast<size_t>(t) * p.ld, e0, p.E, wide, x);
-  float* s_x = reinterpret_cast<float*>(s_val[wave]);
+  float* s_x = reinterpret_cast<float*>(s_val);
 #pragma unroll
   for (int i = 0; i < V; ++i) s_x[e0 + i] = x[i];
 
@@ -572,7 +571,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
   double my_s;
   if (redo) {
     wave_lds_fence();
-    route_exact<V, BF16, SIGMOID>(p, t, l, s_val[wave], my_id, my_s);
+    route_exact<V, BF16, SIGMOID>(p, t, l, s_val, my_id, my_s);
   } else {
     wave_lds_fence();
     const double xj = s_x[max(my_id, 0)];
@@ -581,6 +580,345 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
     my_s = my_id < 0 ? 0.0 : (SIGMOID ? 1.0 / (1.0 + e) : (p.renorm ? e : e / total));
   }
   store_picks(p, o, l, my_id, my_s);
+}
+
+template <int V, bool BF16, bool SIGMOID, bool GROUPS>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wide, int part) {
+  __shared__ double s_val[kWaves][64 * V];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int t = blockIdx.x * kWaves + wave;
+  if (t >= p.T || padding(p, t, static_cast<size_t>(t) * p.k, l)) return;
+  route_token<V, BF16, SIGMOID, GROUPS>(p, t, l, wide, part, s_val[wave]);
+}
+
+// ------------------------------------------------------------ many tokens
+// Four tokens a wave, 16 lanes and 16 V experts each, up to kManyK picks: the steps
+// that a whole wave does for one token (a pick's reduction, the groups' order, the
+// picks' fp64 scores) serve four at once.
+// Here the value and its index in the lane share a key, so that sorting moves one
+// register: the index, counted down, takes the place of the value's lowest bits (up to
+// four), which adds 2^-19 of the value to what is unclear (bf16 logits lose nothing).
+// That is decided as above, the picks with kManyMore that follow them in the token's 16
+// lanes; a row with a NaN or +inf, or with more close values, by the whole wave in
+// fp64.  Loops that few waves run stay rolled: what such a wave waits for, and the
+// launch with it at its end, is mostly their instructions' way into the cache.
+// 16384 tokens, 8 of 256, us: softmax 7.5 (a token a wave 11.9), sigmoids with bias in
+// 8 groups 12 (19); 64 experts 5.0 (9.7) and 8.2 (15).  Bound by VALU instructions and
+// by the waves whose order fp32 leaves open, 3 us of the 12 (with the form above for
+// those 20; all 16 values of a lane anew in fp64 for a border 16).  Where whole tokens
+// are equal sigmoids with a bias, all goes through fp64 (8192 tokens 51 us, above 36).
+constexpr int kManyK = 8, kManyMore = 4;
+static_assert(kManyK + kManyMore <= 16, "a token's candidates are one to a lane");
+// from here on (256 experts, softmax / sigmoids with bias in 8 groups, us: 2048 tokens
+// 4.8 / 7.3, a token a wave 4.1 / 7.5; 4096 tokens 4.9 / 7.4 and 5.1 / 9.0)
+constexpr int kManyTokens = 4096;
+
+// sorted[LO .. LO + N) downwards: Batcher's odd-even merge sort; compile-time indices
+// only, and what nobody reads drops out.
+template <int LO, int N, int R, int V>
+BS_INLINE void merge_keys(uint32_t (&key)[V]) {
+  auto order = [&](int i, int j) {
+    const uint32_t a = key[i], b = key[j];
+    key[i] = max(a, b);
+    key[j] = min(a, b);
+  };
+  if constexpr (2 * R < N) {
+    merge_keys<LO, N, 2 * R>(key);
+    merge_keys<LO + R, N, 2 * R>(key);
+#pragma unroll
+    for (int i = LO + R; i + R < LO + N; i += 2 * R) order(i, i + R);
+  } else {
+    order(LO, LO + R);
+  }
+}
+template <int LO, int N, int V>
+BS_INLINE void sort_keys(uint32_t (&key)[V]) {
+  if constexpr (N > 1) {
+    sort_keys<LO, N / 2>(key);
+    sort_keys<LO + N / 2, N / 2>(key);
+    merge_keys<LO, N, 1>(key);
+  }
+}
+
+// Over the 16 lanes of a token, in all of them.
+#define BS_ROR(v_, n_) __builtin_amdgcn_mov_dpp(static_cast<int>(v_), 0x120 + n_, 0xF, 0xF, true)
+BS_INLINE uint32_t row_kmax(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(BS_ROR(v, 8)));
+  v = max(v, static_cast<uint32_t>(BS_ROR(v, 4)));
+  v = max(v, static_cast<uint32_t>(BS_ROR(v, 2)));
+  return max(v, static_cast<uint32_t>(BS_ROR(v, 1)));
+}
+BS_INLINE float row_fmax(float v) {
+  v = fmaxf(v, __int_as_float(BS_ROR(__float_as_int(v), 8)));
+  v = fmaxf(v, __int_as_float(BS_ROR(__float_as_int(v), 4)));
+  v = fmaxf(v, __int_as_float(BS_ROR(__float_as_int(v), 2)));
+  return fmaxf(v, __int_as_float(BS_ROR(__float_as_int(v), 1)));
+}
+BS_INLINE double row_sum(double v) {
+#define BS_STEP(n_)                                                                                     \
+  {                                                                                                     \
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);                                                 \
+    const uint32_t lo = BS_ROR(b, n_), hi = BS_ROR(b >> 32, n_);                                        \
+    v += __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);                              \
+  }
+  BS_STEP(8)
+  BS_STEP(4)
+  BS_STEP(2)
+  BS_STEP(1)
+#undef BS_STEP
+  return v;
+}
+#undef BS_ROR
+
+template <int V, bool BF16, bool SIGMOID, bool GROUPS>
+__global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, bool wide, bool wide_bias, int part) {
+  constexpr uint32_t kLow = V - 1;
+  constexpr int D = V < kManyK + 1 ? V : kManyK + 1;   // values of a lane that can matter: the picks and the next
+  __shared__ double s_val[kWaves][32 * V];             // logits of the wave's four tokens; then route_exact's
+  __shared__ int s_id[kWaves][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const int r = l >> 4, c = l & 15;                    // the token's row of lanes, the lane in it
+  const int t0 = (blockIdx.x * kWaves + wave) * 4, t = t0 + r;
+  if (t0 >= p.T) return;
+  const bool live = t < p.T && (p.rows == nullptr || t < *p.rows);
+  const float ninf = -__builtin_inff();
+  const int e0 = c * V;
+  float x[V], v[V];
+  float bias[V];
+  if (p.bias != nullptr) load_logits<V, false>(p.bias, 0, e0, p.E, wide_bias, bias);
+  load_logits<V, BF16>(p.logits, static_cast<size_t>(min(t, p.T - 1)) * p.ld, e0, p.E, wide, x);
+  float* s_x = reinterpret_cast<float*>(s_val[wave]) + r * 16 * V;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_x[e0 + i] = x[i];
+
+  const bool by_logit = p.bias == nullptr && (!GROUPS || p.top == 1);
+  float mx = x[0];
+  bool odd = false;
+  uint32_t low = 0u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    odd |= !(x[i] < __builtin_inff());
+    low |= __float_as_uint(x[i]);
+    mx = fmaxf(mx, x[i]);
+  }
+  mx = row_fmax(mx);
+  double total = 1.0;
+  float largest = 1.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = x[i];
+  if (!by_logit || (!SIGMOID && !p.renorm)) {   // (as in route_token)
+    if constexpr (SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + exp_near(fminf(-x[i], 80.0f)));
+    } else {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] = exp_near(fmaxf(x[i] - mx, -100.0f));
+        v[i] = x[i] - mx < -100.0f ? 0.0f : v[i];
+        sum += static_cast<double>(v[i]);
+      }
+      total = row_sum(sum);
+      largest = 1.0f / static_cast<float>(total);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= largest;
+    }
+    if (by_logit) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = x[i];
+    } else if (p.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[i] += bias[i];   // (-inf past E)
+        odd |= !(bias[i] < __builtin_inff());
+      }
+    }
+  }
+  const uint64_t mine = 0xFFFFull << (16 * r);   // the token's lanes
+  bool redo = (__ballot(odd) & mine) != 0;
+  const bool lossy = (__ballot((low & kLow) != 0u) & mine) != 0;
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool off = (x[i] == ninf) | (v[i] == ninf);   // (| : no branch)
+    key[i] = off ? 0u : (key_of(v[i]) & ~kLow) | (kLow - i);
+  }
+  sort_keys<0, V>(key);
+
+  // what decides in fp64: the sum of the scores, and the value of expert e
+  auto exact_total = [&]() {
+    if constexpr (SIGMOID) return 1.0;
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+      const float f = s_x[e0 + i];
+      sum += f == ninf ? 0.0 : exp(static_cast<double>(f) - static_cast<double>(mx));
+    }
+    return row_sum(sum);
+  };
+  auto exact_value = [&](float f, int at, double sum) {
+    const double d = f, b = p.bias != nullptr ? static_cast<double>(p.bias[at]) : 0.0;
+    if (by_logit) return d;
+    if constexpr (SIGMOID) return 1.0 / (1.0 + exp(-d)) + b;
+    else return exp(d - static_cast<double>(mx)) / sum + b;
+  };
+
+  if constexpr (GROUPS) {
+    uint32_t a = key[0], b = key[V > 1 ? 1 : 0];   // the two largest
+    auto join = [&](uint32_t a2, uint32_t b2) {
+      b = max(max(b, b2), min(a, a2));
+      a = max(a, a2);
+    };
+#define BS_JOIN(ctrl_)                                                                                     \
+  join(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), ctrl_, 0xF, 0xF, true)),        \
+       static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), ctrl_, 0xF, 0xF, true)))
+    if (part > 1) BS_JOIN(0xB1);    // lane ^ 1
+    if (part > 2) BS_JOIN(0x4E);    // lane ^ 2
+    if (part > 4) BS_JOIN(0x141);   // the other half of 8
+    if (part > 8) BS_JOIN(0x140);   // the other half of 16
+#undef BS_JOIN
+    const float fa = a == 0u ? ninf : value_of(a & ~kLow), fb = b == 0u ? ninf : value_of(b & ~kLow);
+    const float u = p.top == 2 ? fa + fb : fa;
+    const int g = c / part;
+    int before = 0;
+    for (int h = 0; h < p.groups; ++h) {
+      const float w = __shfl(u, 16 * r + h * part, 64);
+      before += w > u || (w == u && h < g) ? 1 : 0;
+    }
+    const bool here = g < p.groups;
+    if (p.keep < p.groups) {   // the border
+      const float in = row_fmax(here && before == p.keep - 1 ? u : ninf);
+      const float out = row_fmax(here && before == p.keep ? u : ninf);
+      const float terms = p.top == 2 ? fabsf(fa) + fabsf(fb) : fabsf(fa);
+      const float most = row_fmax(here && terms < __builtin_inff() ? terms : 0.0f);
+      // (twice route_token's margin, for the bits that the keys lose)
+      const bool anew = by_logit ? lossy && in == out && in != ninf : !(in - out > 8.0f * kTau * (largest + most));
+      if (__ballot(anew && live && !redo) != 0) {
+        const double sum = exact_total();
+        double da = ninf, db = ninf;
+        auto add = [&](double a2, double b2) {
+          const double lo = a2 > da ? da : a2;
+          da = a2 > da ? a2 : da;
+          db = b2 > db ? b2 : db;
+          db = lo > db ? lo : db;
+        };
+        // (of those that may be among the group's two largest)
+        const float least = fb - 4.0f * kTau * (largest + fabsf(fb));
+        uint32_t which = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) which |= static_cast<uint32_t>(anew & (v[i] >= least) & (v[i] != ninf) & (x[i] != ninf)) << i;
+        while (which != 0u) {
+          const int i = __builtin_ctz(which);
+          which &= which - 1;
+          add(exact_value(s_x[e0 + i], e0 + i, sum), ninf);
+        }
+#pragma unroll 1
+        for (int d = 1; d < part; d <<= 1) add(__shfl_xor(da, d, 64), __shfl_xor(db, d, 64));
+        const double du = p.top == 2 ? da + db : da;
+        int before64 = 0;
+#pragma unroll 1
+        for (int h = 0; h < p.groups; ++h) {
+          const double w = __shfl(du, 16 * r + h * part, 64);
+          before64 += w > du || (w == du && h < g) ? 1 : 0;
+        }
+        before = anew ? before64 : before;
+      }
+    }
+    const bool off = !here || before >= p.keep;
+#pragma unroll
+    for (int i = 0; i < D; ++i) key[i] = off ? 0u : key[i];
+  }
+
+  // the picks: lane j of the token keeps the j-th one's key without its index, its
+  // winner writes its number
+  const uint64_t lower = mine & ((1ull << l) - 1);
+  uint32_t my_key = 0u;
+  int* id = s_id[wave] + 16 * r;
+  int found = 0, wins = 0;
+  auto pick_up_to = [&](int n) {
+    for (; found < n; ++found) {
+      const uint32_t m = row_kmax(key[0]) & ~kLow;
+      const bool tops = key[0] != 0u && (key[0] & ~kLow) == m;
+      const bool won = (__ballot(tops) & lower) == 0 && tops;   // equal ones: the lowest lane
+      if (won) {
+        id[found] = e0 + static_cast<int>(kLow - (key[0] & kLow));
+        ++wins;
+#pragma unroll
+        for (int i = 0; i + 1 < D; ++i) key[i] = key[i + 1];
+        key[D - 1] = 0u;
+      }
+      my_key = c == found ? m : my_key;
+    }
+    return row_kmax(key[0]) & ~kLow;
+  };
+  // (m before n, or the last pick before the best that is left)
+  auto clear = [&](uint32_t m, uint32_t n) {
+    const float fm = value_of(m), fn = value_of(n);
+    return by_logit ? !lossy || m != n : fm - fn > 2.0f * kTau * (largest + fabsf(fm) + fabsf(fn));
+  };
+  bool anew = false;
+  {
+    const uint32_t left = pick_up_to(p.k);
+    const uint32_t next = static_cast<uint32_t>(__shfl_down(static_cast<int>(my_key), 1, 64));
+    const uint32_t below = c == p.k - 1 ? left : next;
+    anew = (__ballot(c < p.k && my_key != 0u && below != 0u && !clear(my_key, below)) & mine) != 0 && live && !redo;
+  }
+  const bool some = __ballot(anew) != 0;
+  double sum64 = 1.0;
+  if (some) {
+    const uint32_t left = pick_up_to(p.k + kManyMore);
+    const uint32_t last = static_cast<uint32_t>(__shfl(static_cast<int>(my_key), 16 * r + p.k - 1, 64));
+    const bool spent = D < V && (__ballot(wins == D) & mine) != 0;
+    redo |= anew && (spent || (left != 0u && !clear(last, left)));
+    if (!by_logit) sum64 = exact_total();
+  }
+  wave_lds_fence();
+  int my_id = my_key != 0u ? id[c] : -1;
+  const double xj = my_id < 0 ? 0.0f : s_x[my_id];
+  const double e = exp(SIGMOID ? -xj : xj - static_cast<double>(mx));
+  double s = my_id < 0 ? 0.0 : (SIGMOID ? 1.0 / (1.0 + e) : (p.renorm ? e : e / total));
+  if (some) {
+    double val = ninf;
+    if (my_id >= 0) {
+      const double b = p.bias != nullptr ? static_cast<double>(p.bias[my_id]) : 0.0;
+      val = by_logit ? xj : (SIGMOID ? s : e / sum64) + b;
+    }
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const double other = __shfl(val, 16 * r + i, 64);
+      const int other_id = __shfl(my_id, 16 * r + i, 64);
+      rank += other > val || (other == val && other_id < my_id) ? 1 : 0;
+    }
+    const int to = 4 * (anew && my_id >= 0 ? 16 * r + rank : l);
+    const uint64_t bits = __builtin_bit_cast(uint64_t, s);
+    const uint32_t lo = __builtin_amdgcn_ds_permute(to, static_cast<int>(bits));
+    const uint32_t hi = __builtin_amdgcn_ds_permute(to, static_cast<int>(bits >> 32));
+    s = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    my_id = __builtin_amdgcn_ds_permute(to, my_id);
+  }
+  const bool there = c < p.k && my_id >= 0;
+  double w = there ? s : 0.0;
+  if (p.renorm) {
+    const double sum = row_sum(w);
+    w = sum == 0.0 ? 0.0 : w / sum;
+  }
+  redo &= live;
+  if (t < p.T && c < p.k && !redo) {
+    const size_t o = static_cast<size_t>(t) * p.k + c;
+    p.ids[o] = live && there ? my_id : -1;
+    p.weights[o] = live && there ? static_cast<float>(w * static_cast<double>(p.scale)) : 0.0f;
+  }
+  uint64_t todo = __ballot(redo && c == 0);
+  while (todo != 0) {
+    const int q = t0 + (__builtin_ctzll(todo) >> 4);
+    todo &= todo - 1;
+    wave_lds_fence();
+    int id64;
+    double s64;
+    route_exact<V / 4, BF16, SIGMOID>(p, q, l, s_val[wave], id64, s64);
+    store_picks(p, static_cast<size_t>(q) * p.k, l, id64, s64);
+  }
 }
 
 struct RouteBwdArgs {
@@ -749,6 +1087,32 @@ int launch_route(const RouteArgs& p, bool bf16, bool sigmoid, bool wide, int par
   }
   return bs_launch_status();
 }
+template <int V, bool GROUPS>
+int launch_many(const RouteArgs& p, bool bf16, bool sigmoid, bool wide, bool wide_bias, int part, hipStream_t st) {
+  const dim3 grid((p.T + 4 * kWaves - 1) / (4 * kWaves)), block(64 * kWaves);
+  if (bf16) {
+    if (sigmoid) k_moe_route_many<V, true, true, GROUPS><<<grid, block, 0, st>>>(p, wide, wide_bias, part);
+    else k_moe_route_many<V, true, false, GROUPS><<<grid, block, 0, st>>>(p, wide, wide_bias, part);
+  } else {
+    if (sigmoid) k_moe_route_many<V, false, true, GROUPS><<<grid, block, 0, st>>>(p, wide, wide_bias, part);
+    else k_moe_route_many<V, false, false, GROUPS><<<grid, block, 0, st>>>(p, wide, wide_bias, part);
+  }
+  return bs_launch_status();
+}
+// Four tokens a wave with V values a lane, if sizes and groups fit it.
+template <int V>
+bool try_many(const RouteArgs& p, bool bf16, bool sigmoid, hipStream_t st, int& status) {
+  if (p.E > 16 * V || p.k > kManyK || p.T < kManyTokens) return false;
+  const int size = p.E / p.groups, part = size / V, b = bf16 ? 2 : 4, bytes = std::min(V * b, 16);
+  const bool wide = p.E % V == 0 && p.ld * b % bytes == 0 && bs_aligned(p.logits, bytes), wide_bias = p.E % V == 0 && bs_aligned(p.bias, 16);
+  if (p.groups == 1) {
+    status = launch_many<V, false>(p, bf16, sigmoid, wide, wide_bias, 16, st);
+    return true;
+  }
+  if (size % V || (part & (part - 1)) || part > 16) return false;
+  status = launch_many<V, true>(p, bf16, sigmoid, wide, wide_bias, part, st);
+  return true;
+}
 // The quick form with V values a lane, if the groups fit it; V and BS_OK or an error
 // in status.
 template <int V>
@@ -810,6 +1174,9 @@ BS_API int moe_route(const void* logits, int64_t ld, int type, const float* bias
   const bool bf16 = type == BS_TYPE_BF16, sigmoid = score == BS_SCORE_SIGMOID;
   hipStream_t st = static_cast<hipStream_t>(stream);
   int status = BS_OK;
+  if (try_many<4>(p, bf16, sigmoid, st, status) || try_many<8>(p, bf16, sigmoid, st, status) ||
+      try_many<16>(p, bf16, sigmoid, st, status))
+    return status;
   if (try_route<1>(p, bf16, sigmoid, st, status) || try_route<2>(p, bf16, sigmoid, st, status) ||
       try_route<4>(p, bf16, sigmoid, st, status) || try_route<8>(p, bf16, sigmoid, st, status))
     return status;
