@@ -1056,9 +1056,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p, b
 #pragma unroll
   for (int i = 0; i < V; ++i) out[i] = d[e0 + i];
   if constexpr (DENSE) {
+    // (a token without a choice has no gradient, whatever its logits hold)
+    const bool any = __ballot(there) != 0;
     const float cf = p.scale;
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = cf * (x[i] * near) * static_cast<float>(static_cast<double>(out[i]) - dot);
+    for (int i = 0; i < V; ++i)
+      out[i] = any ? cf * (x[i] * near) * static_cast<float>(static_cast<double>(out[i]) - dot) : 0.0f;
   }
   store_row<V, BF16>(p.dl, static_cast<size_t>(t) * p.ldd, e0, p.E, wide, out);
 }

@@ -268,6 +268,23 @@ def test_gradient_is_the_slope_of_the_forward(sigmoid, renorm):
         assert abs(num - d[e]) <= tol, (e, float(num), float(d[e]))
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_of_padding_tokens_is_zero(sigmoid, renorm, dtype):
+    """Whatever their logits hold (NaN, infinities) and dweights, rows without a choice get zeros."""
+    x, _ = _logits(3, 9, 40, dtype)
+    x[4:] = math.nan
+    x[5] = math.inf
+    x[6] = -math.inf
+    ids, w = bs.moe_route(x, 4, score=int(sigmoid), renorm=renorm, rows=torch.tensor([4], dtype=torch.int32, device="cuda"))
+    dw = torch.randn((9, 4), generator=torch.Generator().manual_seed(1)).cuda()
+    dw[7] = math.nan
+    d = bs.moe_route_backward(dw, x, ids, score=int(sigmoid), renorm=renorm, dlogits=torch.full_like(x, 7.0))
+    assert not d[4:].any() and d[:4].isfinite().all()
+    _grad_close(d[:4], dw[:4], x[:4], ids[:4], sigmoid, renorm, 1.0)
+
+
 def test_empty():
     x = torch.empty((0, 32), device="cuda")
     ids, w = bs.moe_route(x, 4)
