@@ -546,12 +546,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
 
   // Epilogue: the tile through LDS as bf16, so that a row leaves as whole
   // 16-byte pieces side by side.  A lane's four columns are half a piece; piece
-  // q of a row sits at slot q ^ (row % pieces).
+  // q of a row sits at slot q ^ (row % swap), within runs of swap pieces.
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __syncthreads();       // the stages are done with
   const float* s_as = reinterpret_cast<const float*>(lds + C::kMain);
   const float* s_ws = s_as + BM;
   constexpr int kLanes = BN / 8, kRows = C::kThreads * KG / kLanes;   // pieces of a row, rows at once
+  constexpr int kSwap = kLanes & -kLanes;                             // (a power of two that divides them)
   if (kg == 0) {         // (the other groups have handed their sums over)
 #pragma unroll
     for (int i = 0; i < C::kTN; ++i)
@@ -564,7 +565,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
           const int row = arow[j];
           const float sa = s_as[row];
           const v16i& av = acc[i][j];
-          *reinterpret_cast<uint2*>(lds + row * (BN * 2) + (((col >> 3) ^ (row % kLanes)) << 4) + 8 * (l >> 5)) =
+          *reinterpret_cast<uint2*>(lds + row * (BN * 2) + (((col >> 3) ^ (row % kSwap)) << 4) + 8 * (l >> 5)) =
               uint2{bf16x2_rne(scaled(av[4 * r], sa, sw.x), scaled(av[4 * r + 1], sa, sw.y)),
                     bf16x2_rne(scaled(av[4 * r + 2], sa, sw.z), scaled(av[4 * r + 3], sa, sw.w))};
         }
@@ -575,10 +576,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   // N cuts, value by value
   const bool wide = p.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(p.c) % 16 == 0;
   const int q = tid % kLanes, cols = min(8, N - n0 - 8 * q);
-  if (cols <= 0) return;
+  if (cols <= 0 || tid >= kRows * kLanes) return;
 #pragma unroll 4
   for (int r = tid / kLanes; r < nrows; r += kRows) {
-    const uint4 o = *reinterpret_cast<const uint4*>(lds + r * (BN * 2) + ((q ^ (r % kLanes)) << 4));
+    const uint4 o = *reinterpret_cast<const uint4*>(lds + r * (BN * 2) + ((q ^ (r % kSwap)) << 4));
     uint16_t* dst = p.c + (m0 + r) * p.ldc + n0 + 8 * q;
     if (wide && cols == 8) {
       st_stream16(reinterpret_cast<uint4*>(dst), o);
@@ -713,22 +714,29 @@ int launch_tile(const W8A8Args& p, int64_t wgs, hipStream_t st) {
 // The dense tile shapes and what a launch of each takes, in us: with x = tiles
 // / 256 (one per CU) and R = ceil(x) rounds,
 //   t = start + R * (round + steps * step) + x * steps * load,  steps of 128 of K
-// fitted over 14 row counts from 65 to 4096 at twelve N x K, N = 512 .. 34816 and
+// fitted over 20 row counts from 40 to 6000 at twelve N x K, N = 512 .. 34816 and
 // K = 256 .. 17408, weights pooled past the last-level cache: by least squares,
-// then moved to the least loss by the choice (1.0% behind the best shape in the
-// mean of 168 sizes, at worst 12%).
+// then moved a little to the least loss by the choice (0.6% behind the best shape in
+// the mean of 240 sizes, at worst 13%).  The four shapes with a side of 192 are there
+// for the sizes whose tiles would fill little more than half of the CUs' last round
+// (1024 rows, N = 10240, K = 5120: 54 us, without them 65; 512 rows 43 and 49; 128
+// rows, N = 17408 34 and 40); without them the choice is 2% behind in the mean.
 struct TileShape {
   int bm, bn;
   float start, round, step, load;
 };
 constexpr TileShape kTiles[] = {
-    {256, 256, 0.000f, 6.713f, 1.080f, 0.687f},  // 8 waves of 64 x 128
-    {128, 256, 1.266f, 2.716f, 0.918f, 0.128f},  // 4 waves of 64 x 128, two workgroups a CU
-    {128, 256, 0.000f, 3.739f, 0.859f, 0.188f},  // 8 waves of 64 x 64
-    {128, 128, 0.898f, 2.051f, 0.601f, 0.026f},  // 4 waves of 64 x 64, two workgroups a CU
-    {64, 128, 2.688f, 0.450f, 0.435f, 0.060f},   // 4 waves of 64 x 32, three workgroups a CU
-    {64, 128, 2.483f, 3.453f, 0.371f, 0.000f},   // 2 K groups of 2 waves of 64 x 64
-    {64, 64, 2.096f, 0.434f, 0.216f, 0.069f},    // 4 waves of 32 x 32, K steps of 128, two workgroups a CU
+    {256, 256, 0.000f, 7.046f, 0.966f, 0.691f},  // 8 waves of 64 x 128
+    {128, 256, 1.539f, 2.757f, 0.870f, 0.140f},  // 4 waves of 64 x 128, two workgroups a CU
+    {128, 256, 0.081f, 3.969f, 0.801f, 0.215f},  // 8 waves of 64 x 64
+    {128, 128, 2.219f, 1.504f, 0.561f, 0.093f},  // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 2.069f, 0.579f, 0.451f, 0.000f},   // 4 waves of 64 x 32, three workgroups a CU
+    {64, 128, 1.673f, 3.137f, 0.385f, 0.000f},   // 2 K groups of 2 waves of 64 x 64
+    {64, 64, 2.200f, 0.859f, 0.245f, 0.000f},    // 4 waves of 32 x 32, K steps of 128, two workgroups a CU
+    {192, 256, 0.000f, 6.827f, 0.944f, 0.327f},  // 4 waves of 96 x 128
+    {192, 128, 2.086f, 2.045f, 0.707f, 0.091f},  // 4 waves of 96 x 64, two workgroups a CU
+    {128, 192, 1.067f, 3.429f, 0.601f, 0.166f},  // 4 waves of 64 x 96
+    {64, 192, 1.485f, 4.680f, 0.510f, 0.000f},   // 2 K groups of 2 waves of 64 x 96
 };
 constexpr int kShapes = sizeof(kTiles) / sizeof(kTiles[0]);
 int64_t tiles_of(int i, int M, int N) {
@@ -762,7 +770,11 @@ int run_tiles(int i, const W8A8Args& q, int n0, int n1, hipStream_t st) {
     case 3: return launch_tile<128, 128, 2, 2, 1, 4, 1, 2, false>(p, wgs, st);
     case 4: return launch_tile<64, 128, 1, 4, 1, 4, 1, 3, false>(p, wgs, st);
     case 5: return launch_tile<64, 128, 1, 2, 2, 4, 1, 1, false>(p, wgs, st);
-    default: return launch_tile<64, 64, 2, 2, 1, 4, 2, 2, false>(p, wgs, st);
+    case 6: return launch_tile<64, 64, 2, 2, 1, 4, 2, 2, false>(p, wgs, st);
+    case 7: return launch_tile<192, 256, 2, 2, 1, 3, 1, 1, false>(p, wgs, st);
+    case 8: return launch_tile<192, 128, 2, 2, 1, 3, 1, 2, false>(p, wgs, st);
+    case 9: return launch_tile<128, 192, 2, 2, 1, 4, 1, 1, false>(p, wgs, st);
+    default: return launch_tile<64, 192, 1, 2, 2, 4, 1, 1, false>(p, wgs, st);
   }
 }
 

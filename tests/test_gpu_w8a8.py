@@ -71,6 +71,15 @@ def test_gemm(M, N, K):
     _run(M, N, K)
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (769, 9999, 144), (770, 10000, 256), (513, 15001, 1040),      # 192 x 256
+    (769, 5001, 80), (641, 6000, 128), (191, 17001, 1040),        # 192 x 128
+    (257, 11001, 1040), (301, 11008, 1152), (129, 17001, 1552),   # 128 x 192
+    (65, 17001, 3088), (129, 11008, 3200), (131, 11001, 3088)])   # 64 x 192
+def test_tiles_with_a_side_of_192(M, N, K):
+    _run(M, N, K)
+
+
 def test_largest_sums():
     """K = 131056 of the largest products: the sum is next to 2^31."""
     for M in (1, 20, 70):
