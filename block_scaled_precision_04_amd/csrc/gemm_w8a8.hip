@@ -312,7 +312,7 @@ struct TileCfg {
   static constexpr int kLds = kMain + kScales;
 };
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB, int OCC, bool GROUPED, bool TAIL>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB, int OCC, bool GROUPED, bool TAIL, bool SPLIT>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p, int group_m) {
   using C = TileCfg<BM, BN, WM, WN, KG, STAGES, SUB>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::kLds];
@@ -323,10 +323,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   const int N = p.N, KS = p.KS, NT = (N + 15) >> 4;
   const int n_tiles = (N + BN - 1) / BN;
   // this group's steps of SUB blocks of K: KG * i + kg for i < n_steps
-  const int SS = KS / SUB;
+  // (SPLIT: of the workgroup's run of p.iters of them)
+  static_assert(!SPLIT || (KG == 1 && !GROUPED), "K splits");
+  const int s0 = SPLIT ? static_cast<int>(blockIdx.z) * p.iters : 0;
+  const int SS = SPLIT ? min(p.iters, KS / SUB - s0) : KS / SUB;
   const int n_steps = (SS - kg + KG - 1) / KG, n_turns = (SS + KG - 1) / KG;
 
-  int m0, nrows, nt;
+  int m0, nrows, nt, tile = 0;
   const uint8_t* w = p.w;
   const float* wsc = p.wsc;
   if constexpr (GROUPED) {
@@ -342,6 +345,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
     xcd_tile(blockIdx.x, (p.M + BM - 1) / BM, n_tiles, group_m, mt, nt);
     m0 = mt * BM;
     nrows = min(BM, p.M - m0);
+    tile = mt * n_tiles + nt;
   }
   const int n0 = nt * BN, nt0 = n0 >> 4;
   uint8_t* const glds = lds + kg * C::kGroup;
@@ -351,7 +355,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
   // tile's last and columns past N re-read valid ones; their results are not
   // stored).  Chunks past K re-read the row's last one (TAIL).
   const uint8_t* const a = GROUPED ? p.a : p.a + static_cast<size_t>(m0) * p.lda;
-  w += static_cast<size_t>(nt0) * KS * 1024;
+  w += (static_cast<size_t>(nt0) * KS + s0 * SUB) * 1024;
   uint32_t aoff[C::kAIters], aend[C::kAIters], boff[C::kBIters];
 #pragma unroll
   for (int i = 0; i < C::kAIters; ++i) {
@@ -361,7 +365,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
     if constexpr (GROUPED) src = src_row(p, m0 + src);
     aoff[i] = static_cast<uint32_t>(src) * p.lda;
     aend[i] = aoff[i] + static_cast<uint32_t>(p.K - 16);
-    aoff[i] += static_cast<uint32_t>(16 * swz4(row, q & 3));
+    aoff[i] += static_cast<uint32_t>(16 * swz4(row, q & 3) + s0 * SUB * 64);
   }
 #pragma unroll
   for (int i = 0; i < C::kBIters; ++i)
@@ -544,6 +548,54 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void k_w8a8_tile(W8A8Args p
     }
   }
 
+  // K splits: partial tiles in fragment order through the workspace, as the stream's;
+  // the last workgroup of the tile, whose own sums are still in its registers, adds the
+  // others' and leaves the counter at zero.  (Whole numbers: any order is the same.)
+  if constexpr (SPLIT) {
+    __shared__ int s_last;
+    constexpr int kPart = C::kTN * C::kTM * 16 * 64;
+    const int S = gridDim.z;
+    const size_t stride = static_cast<size_t>(gridDim.x) * C::kWaves * kPart;
+    int* const mine = p.slab + (static_cast<size_t>(tile) * C::kWaves + wave) * kPart + l;
+    {
+      int* dst = mine + blockIdx.z * stride;
+#pragma unroll
+      for (int i = 0; i < C::kTN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kTM; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            __hip_atomic_store(dst + ((i * C::kTM + j) * 16 + r) * 64, acc[i][j][r], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    asm volatile("" ::: "memory");
+    __syncthreads();
+    if (tid == 0)
+      s_last = __hip_atomic_fetch_add(&p.counters[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == S - 1;
+    __syncthreads();
+    if (!s_last) return;
+    for (int z = 0; z < S; ++z) {
+      if (z == static_cast<int>(blockIdx.z)) continue;
+      const int* src = mine + z * stride;
+      v16i x[C::kTN][C::kTM];
+#pragma unroll
+      for (int i = 0; i < C::kTN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kTM; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            x[i][j][r] = __hip_atomic_load(src + ((i * C::kTM + j) * 16 + r) * 64, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int i = 0; i < C::kTN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::kTM; ++j) acc[i][j] += x[i][j];
+    }
+    if (tid == 0) __hip_atomic_store(&p.counters[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+
   // Epilogue: the tile through LDS as bf16, so that a row leaves as whole
   // 16-byte pieces side by side.  A lane's four columns are half a piece; piece
   // q of a row sits at slot q ^ (row % swap), within runs of swap pieces.
@@ -706,8 +758,17 @@ template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB, int OCC, 
 int launch_tile(const W8A8Args& p, int64_t wgs, hipStream_t st) {
   if (wgs > 0x7FFFFFFF) return BS_ERR_SHAPE;
   const dim3 grid(static_cast<uint32_t>(wgs)), block(64 * WM * WN * KG);
-  if (p.K % 128 == 0) k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, false><<<grid, block, 0, st>>>(p, 4);
-  else k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, true><<<grid, block, 0, st>>>(p, 4);
+  if (p.K % 128 == 0) k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, false, false><<<grid, block, 0, st>>>(p, 4);
+  else k_w8a8_tile<BM, BN, WM, WN, KG, STAGES, SUB, OCC, GROUPED, true, false><<<grid, block, 0, st>>>(p, 4);
+  return bs_launch_status();
+}
+// K in runs of p.iters steps, one to a grid layer
+template <int BM, int BN, int WM, int WN, int STAGES, int SUB, int OCC>
+int launch_split(const W8A8Args& p, int64_t wgs, hipStream_t st) {
+  const int steps = p.KS / SUB;
+  const dim3 grid(static_cast<uint32_t>(wgs), 1, (steps + p.iters - 1) / p.iters), block(64 * WM * WN);
+  if (p.K % 128 == 0) k_w8a8_tile<BM, BN, WM, WN, 1, STAGES, SUB, OCC, false, false, true><<<grid, block, 0, st>>>(p, 4);
+  else k_w8a8_tile<BM, BN, WM, WN, 1, STAGES, SUB, OCC, false, true, true><<<grid, block, 0, st>>>(p, 4);
   return bs_launch_status();
 }
 
@@ -716,8 +777,8 @@ int launch_tile(const W8A8Args& p, int64_t wgs, hipStream_t st) {
 //   t = start + R * (round + steps * step) + x * steps * load,  steps of 128 of K
 // fitted over 20 row counts from 40 to 6000 at twelve N x K, N = 512 .. 34816 and
 // K = 256 .. 17408, weights pooled past the last-level cache: by least squares,
-// then moved a little to the least loss by the choice (0.6% behind the best shape in
-// the mean of 240 sizes, at worst 13%).  The four shapes with a side of 192 are there
+// then moved a little, with the K splits' below, to the least loss by the choice (0.4%
+// behind the best in the mean of 344 sizes, at worst 13%).  The four shapes with a side of 192 are there
 // for the sizes whose tiles would fill little more than half of the CUs' last round
 // (1024 rows, N = 10240, K = 5120: 54 us, without them 65; 512 rows 43 and 49; 128
 // rows, N = 17408 34 and 40); without them the choice is 2% behind in the mean.
@@ -727,15 +788,15 @@ struct TileShape {
 };
 constexpr TileShape kTiles[] = {
     {256, 256, 0.000f, 7.046f, 0.966f, 0.691f},  // 8 waves of 64 x 128
-    {128, 256, 1.539f, 2.757f, 0.870f, 0.140f},  // 4 waves of 64 x 128, two workgroups a CU
-    {128, 256, 0.081f, 3.969f, 0.801f, 0.215f},  // 8 waves of 64 x 64
-    {128, 128, 2.219f, 1.504f, 0.561f, 0.093f},  // 4 waves of 64 x 64, two workgroups a CU
-    {64, 128, 2.069f, 0.579f, 0.451f, 0.000f},   // 4 waves of 64 x 32, three workgroups a CU
-    {64, 128, 1.673f, 3.137f, 0.385f, 0.000f},   // 2 K groups of 2 waves of 64 x 64
+    {128, 256, 1.535f, 2.757f, 0.870f, 0.140f},  // 4 waves of 64 x 128, two workgroups a CU
+    {128, 256, 0.081f, 3.969f, 0.778f, 0.215f},  // 8 waves of 64 x 64
+    {128, 128, 2.219f, 1.633f, 0.561f, 0.093f},  // 4 waves of 64 x 64, two workgroups a CU
+    {64, 128, 2.069f, 0.579f, 0.458f, 0.000f},   // 4 waves of 64 x 32, three workgroups a CU
+    {64, 128, 1.673f, 3.132f, 0.376f, 0.000f},   // 2 K groups of 2 waves of 64 x 64
     {64, 64, 2.200f, 0.859f, 0.245f, 0.000f},    // 4 waves of 32 x 32, K steps of 128, two workgroups a CU
     {192, 256, 0.000f, 6.827f, 0.944f, 0.327f},  // 4 waves of 96 x 128
     {192, 128, 2.086f, 2.045f, 0.707f, 0.091f},  // 4 waves of 96 x 64, two workgroups a CU
-    {128, 192, 1.067f, 3.429f, 0.601f, 0.166f},  // 4 waves of 64 x 96
+    {128, 192, 1.066f, 3.426f, 0.601f, 0.166f},  // 4 waves of 64 x 96
     {64, 192, 1.485f, 4.680f, 0.510f, 0.000f},   // 2 K groups of 2 waves of 64 x 96
 };
 constexpr int kShapes = sizeof(kTiles) / sizeof(kTiles[0]);
@@ -753,6 +814,62 @@ int best_tile(int M, int N, int steps) {
   for (int i = 1; i < kShapes; ++i)
     if (tile_cost(i, M, N, steps) < tile_cost(best, M, N, steps)) best = i;
   return best;
+}
+
+// K splits of four of the shapes, through the workspace, where the tiles are too few
+// for the CUs or K is long (M = 128, N = 1024, K = 17408 14.6 us, unsplit 46; N = 5120 33
+// and 49): in S runs of `per` steps a launch takes
+//   scale * t(S * tiles, per steps) + add + mb * (all partials' MB) + kb * (KB that the
+//   last workgroup of a tile adds)
+// fitted over eleven row counts from 65 to 1500 at fourteen N x K, K = 2048 .. 17408
+// (without splits the choice would be 38% behind the best in the mean of those).
+struct SplitCost {
+  int shape;
+  float scale, add, mb, kb;
+};
+constexpr SplitCost kSplits[] = {{2, 1.115f, 1.905f, 0.114f, 0.0106f},
+                                 {3, 1.022f, 0.750f, 0.135f, 0.0142f},
+                                 {4, 0.975f, 1.373f, 0.190f, 0.0197f},
+                                 {6, 1.232f, 0.000f, 0.141f, 0.0392f}};
+struct TileChoice {
+  int shape, per;   // per: steps of 128 of a K run, 0: whole
+  size_t slab;      // bytes of the partials
+};
+TileChoice choose_tile(int M, int N, int steps) {
+  TileChoice best{best_tile(M, N, steps), 0, 0};
+  if (steps < 8 || tiles_of(2, M, N) > 400) return best;
+  float least = tile_cost(best.shape, M, N, steps);
+  for (const SplitCost& c : kSplits) {
+    const TileShape& t = kTiles[c.shape];
+    const int64_t tiles = tiles_of(c.shape, M, N);
+    int last = 0;
+    for (int s : {2, 3, 4, 5, 6, 8, 10, 12, 16, 24}) {
+      const int per = (steps + s - 1) / s, S = (steps + per - 1) / per;
+      if (per < 4 || S * tiles > 800) break;
+      if (per == last) continue;
+      last = per;
+      const float x = static_cast<float>(S * tiles) / 256.0f, kb = static_cast<float>(t.bm * t.bn) * 0.004f;
+      const float cost = c.scale * (t.start + std::ceil(x) * (t.round + per * t.step) + x * per * t.load) + c.add +
+                         c.mb * kb * 0.001f * static_cast<float>(S * tiles) + c.kb * kb * static_cast<float>(S - 1);
+      if (cost < least) {
+        least = cost;
+        best = TileChoice{c.shape, per, static_cast<size_t>(S * tiles) * t.bm * t.bn * sizeof(int)};
+      }
+    }
+  }
+  return best;
+}
+int run_split(const TileChoice& c, W8A8Args& p, void* ws, hipStream_t st) {
+  p.counters = static_cast<int*>(ws);
+  p.slab = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
+  p.iters = c.shape == 6 ? c.per : 2 * c.per;   // (steps of 128 there, of 64 else)
+  const int64_t wgs = tiles_of(c.shape, p.M, p.N);
+  switch (c.shape) {
+    case 2: return launch_split<128, 256, 2, 4, 4, 1, 1>(p, wgs, st);
+    case 3: return launch_split<128, 128, 2, 2, 4, 1, 2>(p, wgs, st);
+    case 4: return launch_split<64, 128, 1, 4, 4, 1, 3>(p, wgs, st);
+    default: return launch_split<64, 64, 2, 2, 4, 2, 2>(p, wgs, st);
+  }
 }
 
 // columns [n0, n1) of the problem as tiles of shape i; n0 is a multiple of 16
@@ -781,8 +898,11 @@ int run_tiles(int i, const W8A8Args& q, int n0, int n1, hipStream_t st) {
 // One shape for all columns; or, where the large tiles would end in a partial
 // round, large tiles over as many columns as whole rounds take and the rest as
 // the shape that is quickest there (the second launch costs about 1 us more).
-int run_dense_tile(const W8A8Args& p, hipStream_t st) {
-  const int steps = p.KS / 2, b = best_tile(p.M, p.N, steps);
+int run_dense_tile(W8A8Args& p, void* ws, hipStream_t st) {
+  const int steps = p.KS / 2;
+  const TileChoice c = choose_tile(p.M, p.N, steps);
+  if (c.per > 0) return run_split(c, p, ws, st);
+  const int b = c.shape;
   const int64_t mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
   const int64_t rounds = mt * nt / 256;
   if (rounds >= 1) {
@@ -802,7 +922,10 @@ int run_dense_tile(const W8A8Args& p, hipStream_t st) {
 
 size_t bs_w8a8_workspace(int M, int N, int K) {
   const int KS = (K + 127) / 128 * 2;
-  if (!use_stream(M, N, KS)) return 0;
+  if (!use_stream(M, N, KS)) {
+    const TileChoice c = choose_tile(M, N, KS / 2);
+    return c.per > 0 ? kWsCounterBytes + c.slab : 0;
+  }
   const StreamCfg d = dense_stream_cfg(M, N, KS);
   return d.s > 1 ? kWsCounterBytes + stream_slab(d) : 0;
 }
@@ -821,7 +944,7 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
   p.N = N;
   p.K = K;
   p.KS = (K + 127) / 128 * 2;
-  return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, st);
+  return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, ws, st);
 }
 
 // Row tiles by S / E, the rows an expert would have if they were spread evenly

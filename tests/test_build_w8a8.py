@@ -7,7 +7,7 @@ checks of spills and M0 cover every source already).
   too early.
 * Tiles: the waits of the K loop leave the loads of later steps in flight, and the
   loads sit between the MFMAs of a half step.
-* K splits of the stream: the hand-off through the workspace uses device-scope
+* K splits of the stream and of tiles: the hand-off through the workspace uses device-scope
   stores and loads, acknowledged before the counter is raised."""
 import re
 
@@ -63,9 +63,9 @@ def test_tile_loop_keeps_loads_in_flight():
     assert seen >= 20, seen
 
 
-def test_stream_split_handoff():
+def test_split_handoff():
     seen = 0
-    for name, ins, _ in _named(r"k_w8a8_streamILi\d+ELi\d+ELi\d+ELb[01]ELb0E"):
+    for name, ins, _ in _named(r"k_w8a8_streamILi\d+ELi\d+ELi\d+ELb[01]ELb0E|k_w8a8_tileI(Li\d+E)+Lb0ELb[01]ELb1E"):
         a = next(i for i, s in enumerate(ins) if s.startswith("global_atomic_add"))
         dev = [i for i, s in enumerate(ins[:a]) if s.startswith("global_store") and re.search(r"\bsc1\b", s)]
         assert dev, name
@@ -74,4 +74,4 @@ def test_stream_split_handoff():
         assert any(s.startswith("global_load") and re.search(r"\bsc1\b", s) for s in ins[a + 1:]), name
         assert not any(s.startswith(("buffer_wbl2", "buffer_inv")) for s in ins), name
         seen += 1
-    assert seen >= 10, seen
+    assert seen >= 18, seen

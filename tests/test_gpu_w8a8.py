@@ -80,6 +80,59 @@ def test_tiles_with_a_side_of_192(M, N, K):
     _run(M, N, K)
 
 
+SPLIT = [(257, 4099, 12304), (257, 4099, 12288), (300, 4096, 12288),      # 128 x 256, the last 64 x 128
+         (65, 9999, 4112), (128, 10240, 17408), (513, 2053, 4112),      # 128 x 128
+         (65, 3001, 8208), (129, 2053, 8208), (72, 5120, 8192),       # 64 x 128
+         (65, 33, 2064), (129, 33, 2064), (100, 1024, 17408), (70, 17, 131056)]   # 64 x 64
+
+
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_tiles_with_k_split(M, N, K):
+    assert bs.workspace_bytes(bs.BS_OP_W8A8_INT8, M, N, K) > 0
+    _run(M, N, K)
+
+
+def test_one_workspace_for_calls_in_turn():
+    """Streams and tiles of several splits through one buffer, twice round, and once
+    captured and replayed: the counters are back at zero every time."""
+    jobs, need = [], 0
+    for M, N, K in ((8, 64, 17408), (65, 33, 2064), (129, 2053, 8208), (40, 512, 12288), (513, 2053, 4112), (70, 16, 16384)):
+        a, w = _codes(M, (M, K)), _codes(N, (N, K))
+        sa, sw = _scales(3, M), _scales(4, N)
+        pre, desc = bs.prelayout_int8(_dev(w))
+        need = max(need, bs.workspace_bytes(bs.BS_OP_W8A8_INT8, M, N, K))
+        jobs.append((_dev(a), _dev(sa), desc, pre, _dev(sw), torch.empty((M, N), dtype=torch.bfloat16, device="cuda"),
+                     int8.gemm(a, sa, w, sw)))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def run():
+        for a, sa, desc, pre, sw, c, _ in jobs:
+            bs.bsgemm_w8a8_int8(a, sa, desc, pre, sw, out=c, ws=ws)
+
+    def check():
+        torch.cuda.synchronize()
+        for *_, c, want in jobs:
+            assert np.array_equal(host_bits16(c), want)
+            c.fill_(3.0)
+        assert not ws[:65536].any()
+    for _ in range(2):
+        run()
+        check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for _ in range(4):
+        graph.replay()
+        check()
+        run()
+        check()
+
+
 def test_largest_sums():
     """K = 131056 of the largest products: the sum is next to 2^31."""
     for M in (1, 20, 70):
