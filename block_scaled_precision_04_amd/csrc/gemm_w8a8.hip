@@ -292,7 +292,8 @@ __global__ __launch_bounds__(1024) void k_w8a8_stream(W8A8Args p) {
 //
 // KG > 1: that many groups of WM x WN waves share the tile, each over every
 // KG-th step with buffers of its own, and their partial sums are added through
-// LDS.  TAIL: K is no multiple of 128.
+// LDS.  SPLIT: the grid's layers share a tile, each a run of K.  TAIL: K is no multiple
+// of 128.
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int SUB>
 struct TileCfg {
   static_assert(STAGES >= 2 && STAGES <= 4 && (SUB == 1 || SUB == 2), "the K loop");
