@@ -606,7 +606,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
 // 8 groups 12 (19); 64 experts 5.0 (9.7) and 8.2 (15).  Bound by VALU instructions and
 // by the waves whose order fp32 leaves open, 3 us of the 12 (with the form above for
 // those 20; all 16 values of a lane anew in fp64 for a border 16).  Where whole tokens
-// are equal sigmoids with a bias, all goes through fp64 (8192 tokens 51 us, above 36).
+// are equal sigmoids with a bias, all goes through fp64 (8192 tokens 51 us, a token a
+// wave 36).
 constexpr int kManyK = 8, kManyMore = 4;
 static_assert(kManyK + kManyMore <= 16, "a token's candidates are one to a lane");
 // from here on (256 experts, softmax / sigmoids with bias in 8 groups, us: 2048 tokens
@@ -973,7 +974,7 @@ BS_INLINE void store_row(void* base, size_t row, int e0, int E, bool wide, const
 // where an expert is there twice, one after the other, in the order of j.  Only a
 // softmax over all experts needs the row's logits (DENSE), the others those of the
 // choices.  Bound by the rows' stores and launch (16384 x 256 fp32, 8 choices: 16.8
-// MB written).
+// MB written, 8 us).
 template <int V, bool BF16, bool SIGMOID, bool DENSE>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p, bool wide) {
   __shared__ __attribute__((aligned(16))) float s_d[kWaves][64 * V];
