@@ -150,6 +150,15 @@ BS_INLINE void xcd_tile(int b, int m_tiles, int n_tiles, int group_m, int& mt, i
 constexpr size_t kWsCounterBytes = 64 * 1024;
 constexpr int kWsMaxCounters = static_cast<int>(kWsCounterBytes / sizeof(int));
 
+// How the dense W8A8 GEMM runs a size (found once a call: some 0.6 us on the host):
+// as a weight stream, or as tiles of a shape in K runs of `per` steps (0: whole); ws:
+// bytes of workspace.
+struct W8A8Plan {
+  bool stream;
+  int shape, per;
+  size_t ws;
+};
+
 // Split-K reduction of the last-arriving workgroup: sum[v] = the S partials
 // base[b * stride + v * VSTRIDE] (fp32, or int32 where the sums are whole)
 // added in split order b = 0, 1, ... (deterministic).  The partials were written with device-scope stores, so

@@ -26,11 +26,11 @@ int bs_launch_w4a4_grouped(const uint8_t* a, int64_t lda, const uint8_t* as, int
                            int64_t ldc, int S, int Ma, int E, int N, int K, hipStream_t st);
 size_t bs_w4a4_workspace(int M, int N, int K);
 int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t* w, const float* wsc, uint16_t* c,
-                   int64_t ldc, int M, int N, int K, void* ws, hipStream_t st);
+                   int64_t ldc, int M, int N, int K, const W8A8Plan& plan, void* ws, hipStream_t st);
 int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const int* offsets, const int* rows,
                            const uint8_t* w, size_t w_stride, const float* wsc, uint16_t* c, int64_t ldc, int S,
                            int Ma, int E, int N, int K, hipStream_t st);
-size_t bs_w8a8_workspace(int M, int N, int K);
+W8A8Plan bs_w8a8_plan(int M, int N, int K);
 size_t bs_moe_sort_workspace(int T, int k, int E);
 
 namespace {
@@ -113,7 +113,7 @@ BS_API size_t bs_workspace_bytes(int op, int M, int N, int K) {
   }
   if (op == BS_OP_W8A8_INT8) {
     if (M < 1 || M > (1 << 22) || !i8_shape_ok(N, K)) return 0;
-    return bs_w8a8_workspace(M, N, K);
+    return bs_w8a8_plan(M, N, K).ws;
   }
   if (op == BS_OP_MOE_SORT) return bs_moe_sort_workspace(M, N, K);
   return 0;
@@ -263,10 +263,11 @@ BS_API int bsgemm_w8a8_int8(const void* a, int64_t lda, const float* a_scale, co
                bs_aligned(w_scale, 4),
            BS_ERR_ALIGN);
   BS_CHECK(lda < (1 << 24), BS_ERR_SHAPE);  // the 256 rows of a tile are addressed with 32-bit offsets
-  const int wst = check_workspace(bs_w8a8_workspace(M, N, K), ws, ws_bytes);
+  const W8A8Plan plan = bs_w8a8_plan(M, N, K);
+  const int wst = check_workspace(plan.ws, ws, ws_bytes);
   if (wst != BS_OK) return wst;
   return bs_launch_w8a8(static_cast<const uint8_t*>(a), lda, a_scale, static_cast<const uint8_t*>(w_pre), w_scale,
-                        static_cast<uint16_t*>(c), ldc, M, N, K, ws, static_cast<hipStream_t>(stream));
+                        static_cast<uint16_t*>(c), ldc, M, N, K, plan, ws, static_cast<hipStream_t>(stream));
 }
 
 BS_API int bsgemm_w8a8_int8_grouped(const void* a, int64_t lda, const float* a_scale, int Ma, const int32_t* offsets,

@@ -832,12 +832,8 @@ constexpr SplitCost kSplits[] = {{2, 1.115f, 1.905f, 0.114f, 0.0106f},
                                  {3, 1.022f, 0.750f, 0.135f, 0.0142f},
                                  {4, 0.975f, 1.373f, 0.190f, 0.0197f},
                                  {6, 1.232f, 0.000f, 0.141f, 0.0392f}};
-struct TileChoice {
-  int shape, per;   // per: steps of 128 of a K run, 0: whole
-  size_t slab;      // bytes of the partials
-};
-TileChoice choose_tile(int M, int N, int steps) {
-  TileChoice best{best_tile(M, N, steps), 0, 0};
+W8A8Plan choose_tile(int M, int N, int steps) {
+  W8A8Plan best{false, best_tile(M, N, steps), 0, 0};
   if (steps < 8 || tiles_of(2, M, N) > 400) return best;
   float least = tile_cost(best.shape, M, N, steps);
   for (const SplitCost& c : kSplits) {
@@ -854,13 +850,13 @@ TileChoice choose_tile(int M, int N, int steps) {
                          c.mb * kb * 0.001f * static_cast<float>(S * tiles) + c.kb * kb * static_cast<float>(S - 1);
       if (cost < least) {
         least = cost;
-        best = TileChoice{c.shape, per, static_cast<size_t>(S * tiles) * t.bm * t.bn * sizeof(int)};
+        best = W8A8Plan{false, c.shape, per, kWsCounterBytes + static_cast<size_t>(S * tiles) * t.bm * t.bn * sizeof(int)};
       }
     }
   }
   return best;
 }
-int run_split(const TileChoice& c, W8A8Args& p, void* ws, hipStream_t st) {
+int run_split(const W8A8Plan& c, W8A8Args& p, void* ws, hipStream_t st) {
   p.counters = static_cast<int*>(ws);
   p.slab = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kWsCounterBytes);
   p.iters = c.shape == 6 ? c.per : 2 * c.per;   // (steps of 128 there, of 64 else)
@@ -899,9 +895,8 @@ int run_tiles(int i, const W8A8Args& q, int n0, int n1, hipStream_t st) {
 // One shape for all columns; or, where the large tiles would end in a partial
 // round, large tiles over as many columns as whole rounds take and the rest as
 // the shape that is quickest there (the second launch costs about 1 us more).
-int run_dense_tile(W8A8Args& p, void* ws, hipStream_t st) {
+int run_dense_tile(const W8A8Plan& c, W8A8Args& p, void* ws, hipStream_t st) {
   const int steps = p.KS / 2;
-  const TileChoice c = choose_tile(p.M, p.N, steps);
   if (c.per > 0) return run_split(c, p, ws, st);
   const int b = c.shape;
   const int64_t mt = (p.M + 255) / 256, nt = (p.N + 255) / 256;
@@ -921,18 +916,15 @@ int run_dense_tile(W8A8Args& p, void* ws, hipStream_t st) {
 
 }  // namespace
 
-size_t bs_w8a8_workspace(int M, int N, int K) {
+W8A8Plan bs_w8a8_plan(int M, int N, int K) {
   const int KS = (K + 127) / 128 * 2;
-  if (!use_stream(M, N, KS)) {
-    const TileChoice c = choose_tile(M, N, KS / 2);
-    return c.per > 0 ? kWsCounterBytes + c.slab : 0;
-  }
+  if (!use_stream(M, N, KS)) return choose_tile(M, N, KS / 2);
   const StreamCfg d = dense_stream_cfg(M, N, KS);
-  return d.s > 1 ? kWsCounterBytes + stream_slab(d) : 0;
+  return W8A8Plan{true, 0, 0, d.s > 1 ? kWsCounterBytes + stream_slab(d) : 0};
 }
 
 int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t* w, const float* wsc, uint16_t* c,
-                   int64_t ldc, int M, int N, int K, void* ws, hipStream_t st) {
+                   int64_t ldc, int M, int N, int K, const W8A8Plan& plan, void* ws, hipStream_t st) {
   W8A8Args p{};
   p.a = a;
   p.as = as;
@@ -945,7 +937,7 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
   p.N = N;
   p.K = K;
   p.KS = (K + 127) / 128 * 2;
-  return use_stream(M, N, p.KS) ? run_dense_stream(p, ws, st) : run_dense_tile(p, ws, st);
+  return plan.stream ? run_dense_stream(p, ws, st) : run_dense_tile(plan, p, ws, st);
 }
 
 // Row tiles by S / E, the rows an expert would have if they were spread evenly
