@@ -265,6 +265,13 @@ BS_INLINE float exp_near(float d) {
   return fmaf(e, lo * 0.693147181f, e);
 }
 
+// The sigmoid to within kTau.  Outside of [-80, 100] it is 0 or 1 to within that, and
+// there the product in exp_near passes fp32 for x from 2.36e38 on (its error term is
+// then infinite too, and the result a NaN).
+BS_INLINE float sigmoid_near(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_near(__builtin_amdgcn_fmed3f(-x, -100.0f, 80.0f)));
+}
+
 // e^(x - mx) to about an ulp and a half: the rounding error of the difference (which
 // would cost |x - mx| / 2 ulps) and the rest of log2(e) go the same way.
 BS_INLINE float exp_diff(float x, float mx) {
@@ -377,9 +384,7 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        // (below -80 the score is 0 to within kTau)
-        const float e = exp_near(fminf(-x[i], 80.0f));
-        v[i] = __builtin_amdgcn_rcpf(1.0f + e);
+        v[i] = sigmoid_near(x[i]);
       }
     } else {
       double part_sum = 0.0;
@@ -710,7 +715,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
   if (!by_logit || (!SIGMOID && !p.renorm)) {   // (as in route_token)
     if constexpr (SIGMOID) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + exp_near(fminf(-x[i], 80.0f)));
+      for (int i = 0; i < V; ++i) v[i] = sigmoid_near(x[i]);
     } else {
       double sum = 0.0;
 #pragma unroll
