@@ -80,20 +80,28 @@ BS_INLINE void route_exact(const RouteArgs& p, int t, int l, double* s_val, int&
 #pragma unroll
     for (int i = 0; i < V; ++i) sc[i] = bad ? __builtin_nan("") : sc[i] / sum;
   }
-  // the order: by logits where nothing is added to the scores and none summed
-  const bool by_logit = p.bias == nullptr && (p.groups == 1 || p.top == 1);
+  // the order of experts: by logits where nothing is added to the scores
+  const bool by_logit = p.bias == nullptr;
+  auto order = [&](int i, double v) {
+    v = v != v ? kNanValue : v;
+    return x[i] == ninf || 64 * i + l >= p.E ? ninf : v;
+  };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = 64 * i + l;
-    const double b = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0;
-    double v = by_logit ? x[i] : sc[i] + b;
-    v = v != v ? kNanValue : v;
-    val[i] = x[i] == ninf || e >= p.E ? ninf : v;
+    const double b = !by_logit && e < p.E ? p.bias[e] : 0.0;
+    val[i] = order(i, by_logit ? x[i] : sc[i] + b);
   }
   if (p.groups > 1) {
-    // 64 / G2 lanes to a group (G2: groups rounded up to a power of two)
+    // 64 / G2 lanes to a group (G2: groups rounded up to a power of two); a sum of two
+    // is one of scores
+    if (by_logit && p.top == 2) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_val[64 * i + l] = val[i];
+      for (int i = 0; i < V; ++i) s_val[64 * i + l] = order(i, sc[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s_val[64 * i + l] = val[i];
+    }
     wave_lds_fence();
     const int size = p.E / p.groups;
     int part = 64;
@@ -337,8 +345,8 @@ BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wid
 }
 
 // The quick form: V consecutive experts a lane, the choice by fp32 values.  Without a
-// bias (and with groups of group_top 1) these are the logits themselves, and the
-// order is exact.  Else they are scores within kTau of the real ones; where two
+// bias these are the logits themselves (groups' sums of two aside), and the order is
+// exact.  Else they are scores within kTau of the real ones; where two
 // values that the order or the border hangs on are closer than that (about one token
 // in 200 of 256 sigmoids), what is close is decided by fp64 values: the groups' sums
 // all anew, or the picks together with up to kMore that follow them, ranked.  (The
@@ -365,7 +373,8 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
 #pragma unroll
   for (int i = 0; i < V; ++i) s_x[e0 + i] = x[i];
 
-  const bool by_logit = p.bias == nullptr && (!GROUPS || p.top == 1);
+  const bool by_logit = p.bias == nullptr;                      // experts
+  const bool by_score = !by_logit || (GROUPS && p.top == 2);    // groups
   float mx = x[0];
   bool odd = false;
 #pragma unroll
@@ -377,7 +386,7 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
   mx = wave_fmax(mx);
   double total = 1.0;     // softmax: the sum of exp(x - mx)
   float largest = 1.0f;   // of the scores
-  const bool scored = !by_logit || (!SIGMOID && !p.renorm);
+  const bool scored = by_score || (!SIGMOID && !p.renorm);
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = x[i];
   if (scored) {
@@ -401,7 +410,7 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (by_logit) {
+      if (!by_score) {
         v[i] = x[i];
       } else {
         if (p.bias != nullptr) {
@@ -430,12 +439,22 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
   };
   int my_id = -1;
   if (!redo) {
-    uint32_t key[V];
+    uint32_t key[V], ga = 0u, gb = 0u;   // (ga, gb: the two largest scores where the keys are logits)
     int id[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       key[i] = v[i] == ninf ? 0u : key_of(v[i]);
       id[i] = e0 + i;
+    }
+    if constexpr (GROUPS) {
+      if (by_logit && by_score) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          gb = max(gb, min(ga, key[i]));
+          ga = max(ga, key[i]);
+          key[i] = v[i] == ninf ? 0u : key_of(x[i]);
+        }
+      }
     }
     // each list sorted: downwards, equal ones in the order of their index (only
     // neighbours change places)
@@ -462,6 +481,10 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
         a = max(a, a2);
       };
       if constexpr (NL == 2) join(key[NL == 2 ? 4 : 0], key[NL == 2 ? 5 : 0]);
+      if (by_logit && by_score) {
+        a = ga;
+        b = gb;
+      }
 #define BS_JOIN(ctrl_)                                                                                     \
   join(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), ctrl_, 0xF, 0xF, true)),        \
        static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), ctrl_, 0xF, 0xF, true)))
@@ -482,7 +505,7 @@ BS_INLINE void route_token(const RouteArgs& p, int t, int l, bool wide, int part
         before += w > u || (w == u && h < g) ? 1 : 0;
       }
       const bool here = g < p.groups;
-      if (p.keep < p.groups && !by_logit) {   // the border
+      if (p.keep < p.groups && by_score) {   // the border
         const float in = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep - 1)));
         const float out = lane_of(u, __builtin_ctzll(__ballot(here && before == p.keep)));
         // (a sum is off by what its terms are, and those of any group may be large ones
@@ -697,7 +720,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
 #pragma unroll
   for (int i = 0; i < V; ++i) s_x[e0 + i] = x[i];
 
-  const bool by_logit = p.bias == nullptr && (!GROUPS || p.top == 1);
+  const bool by_logit = p.bias == nullptr;                      // (as in route_token)
+  const bool by_score = !by_logit || (GROUPS && p.top == 2);
   float mx = x[0];
   bool odd = false;
   uint32_t low = 0u;
@@ -712,7 +736,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
   float largest = 1.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = x[i];
-  if (!by_logit || (!SIGMOID && !p.renorm)) {   // (as in route_token)
+  if (by_score || (!SIGMOID && !p.renorm)) {
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = sigmoid_near(x[i]);
@@ -729,7 +753,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] *= largest;
     }
-    if (by_logit) {
+    if (!by_score) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = x[i];
     } else if (p.bias != nullptr) {
@@ -743,11 +767,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
   const uint64_t mine = 0xFFFFull << (16 * r);   // the token's lanes
   bool redo = (__ballot(odd) & mine) != 0;
   const bool lossy = (__ballot((low & kLow) != 0u) & mine) != 0;
-  uint32_t key[V];
+  uint32_t key[V], ga = 0u, gb = 0u;   // (as in route_token)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const bool off = (x[i] == ninf) | (v[i] == ninf);   // (| : no branch)
     key[i] = off ? 0u : (key_of(v[i]) & ~kLow) | (kLow - i);
+  }
+  if constexpr (GROUPS) {
+    if (by_logit && by_score) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        gb = max(gb, min(ga, key[i]));
+        ga = max(ga, key[i]);
+        key[i] = x[i] == ninf ? 0u : (key_of(x[i]) & ~kLow) | (kLow - i);
+      }
+    }
   }
   sort_keys<0, V>(key);
 
@@ -764,7 +798,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
   };
   auto exact_value = [&](float f, int at, double sum) {
     const double d = f, b = p.bias != nullptr ? static_cast<double>(p.bias[at]) : 0.0;
-    if (by_logit) return d;
+    if (!by_score) return d;
     if constexpr (SIGMOID) return 1.0 / (1.0 + exp(-d)) + b;
     else return exp(d - static_cast<double>(mx)) / sum + b;
   };
@@ -775,6 +809,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
       b = max(max(b, b2), min(a, a2));
       a = max(a, a2);
     };
+    if (by_logit && by_score) {
+      a = ga;
+      b = gb;
+    }
 #define BS_JOIN(ctrl_)                                                                                     \
   join(static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), ctrl_, 0xF, 0xF, true)),        \
        static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), ctrl_, 0xF, 0xF, true)))
@@ -798,7 +836,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route_many(RouteArgs p, boo
       const float terms = p.top == 2 ? fabsf(fa) + fabsf(fb) : fabsf(fa);
       const float most = row_fmax(here && terms < __builtin_inff() ? terms : 0.0f);
       // (twice route_token's margin, for the bits that the keys lose)
-      const bool anew = by_logit ? lossy && in == out && in != ninf : !(in - out > 8.0f * kTau * (largest + most));
+      const bool anew = by_score ? !(in - out > 8.0f * kTau * (largest + most)) : lossy && in == out && in != ninf;
       if (__ballot(anew && live && !redo) != 0) {
         const double sum = exact_total();
         double da = ninf, db = ninf;

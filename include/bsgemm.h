@@ -490,8 +490,9 @@ BS_API int dequant_int8(const void* q, const float* scale, void* out, int M, int
  *   weights[t, j]  scale * s[ids], divided by the sum of the chosen s with renorm
  *                  != 0 (0 where that sum is 0); 0 for -1
  * Equal v, and groups that count the same, in the order of their index.  Scores
- * and their sums are compared in 64 bits (without a bias, experts by their
- * logits), so ids are the definition's.  A NaN v, or a group's NaN, comes after
+ * and their sums are compared in 64 bits.  Without a bias experts are compared by
+ * their logits, whatever group_top is (so also where their scores are equal
+ * numbers, as sigmoids from 37 on), and so are groups with group_top 1.  A NaN v, or a group's NaN, comes after
  * every number; weights of a softmax over a NaN or +inf are NaN.
  * logits: fp32 or bf16 (type BS_TYPE_F32, BS_TYPE_BF16) [T, E], ld elements, ld
  * >= E; bias: fp32 [E] or NULL (it is not part of the weights).  rows: NULL, or

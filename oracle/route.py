@@ -30,14 +30,16 @@ def route(logits, k, bias=None, sigmoid=False, groups=1, topk_groups=1, group_to
     size = E // groups
     for t in range(T if live is None else min(max(live, 0), T)):
         s = scores(logits[t], sigmoid)
-        plain = bias is None and (groups == 1 or group_top == 1)
-        v = logits[t] if plain else s + (0.0 if bias is None else np.asarray(bias, np.float64))
-        v = [-math.inf if logits[t, e] == -math.inf else (-1e300 if math.isnan(v[e]) else float(v[e])) for e in range(E)]
+        def order(v):
+            return [-math.inf if logits[t, e] == -math.inf else (-1e300 if math.isnan(v[e]) else float(v[e])) for e in range(E)]
+        # without a bias experts go by their logits, and groups too where one expert stands for each
+        v = order(logits[t] if bias is None else s + np.asarray(bias, np.float64))
+        of_group = order(s) if bias is None and group_top > 1 else v
         on = list(range(E))
         if groups > 1:
             count = []
             for g in range(groups):
-                best = sorted(v[g * size:(g + 1) * size], reverse=True)[:group_top]
+                best = sorted(of_group[g * size:(g + 1) * size], reverse=True)[:group_top]
                 c = sum(best)
                 count.append(-1e300 if math.isnan(c) else c)
             kept = sorted(range(groups), key=lambda g: (-count[g], g))[:topk_groups]
