@@ -65,43 +65,36 @@ BS_INLINE void route_exact(const RouteArgs& p, int t, int l, double* s_val, int&
     mx = x[i] > mx ? x[i] : mx;
   }
   bad = __ballot(bad) != 0;
+  double total = 1.0;   // softmax: the sum of exp(x - mx)
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < V; ++i) sc[i] = 1.0 / (1.0 + exp(-x[i]));
   } else {
     mx = wave_max_f64(mx);
-    double sum = 0.0;
+    total = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       sc[i] = x[i] == ninf ? 0.0 : exp(x[i] - mx);
-      sum += sc[i];
+      total += sc[i];
     }
-    sum = wave_sum_f64(sum);
+    total = wave_sum_f64(total);
 #pragma unroll
-    for (int i = 0; i < V; ++i) sc[i] = bad ? __builtin_nan("") : sc[i] / sum;
+    for (int i = 0; i < V; ++i) sc[i] = bad ? __builtin_nan("") : sc[i] / total;
   }
   // the order of experts: by logits where nothing is added to the scores
   const bool by_logit = p.bias == nullptr;
-  auto order = [&](int i, double v) {
-    v = v != v ? kNanValue : v;
-    return x[i] == ninf || 64 * i + l >= p.E ? ninf : v;
-  };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = 64 * i + l;
-    const double b = !by_logit && e < p.E ? p.bias[e] : 0.0;
-    val[i] = order(i, by_logit ? x[i] : sc[i] + b);
+    const double b = p.bias != nullptr && e < p.E ? p.bias[e] : 0.0;
+    double v = by_logit ? x[i] : sc[i] + b;
+    v = v != v ? kNanValue : v;
+    val[i] = x[i] == ninf || e >= p.E ? ninf : v;
   }
   if (p.groups > 1) {
-    // 64 / G2 lanes to a group (G2: groups rounded up to a power of two); a sum of two
-    // is one of scores
-    if (by_logit && p.top == 2) {
+    // 64 / G2 lanes to a group (G2: groups rounded up to a power of two)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s_val[64 * i + l] = order(i, sc[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s_val[64 * i + l] = val[i];
-    }
+    for (int i = 0; i < V; ++i) s_val[64 * i + l] = val[i];
     wave_lds_fence();
     const int size = p.E / p.groups;
     int part = 64;
@@ -124,6 +117,15 @@ BS_INLINE void route_exact(const RouteArgs& p, int t, int l, double* s_val, int&
       a = a2 > a ? a2 : a;
       b = b2 > b ? b2 : b;
       b = lo > b ? lo : b;
+    }
+    if (by_logit && p.top == 2) {   // (a sum is one of scores)
+      auto score = [&](double v) {
+        if (!(v > kNanValue)) return v;
+        if constexpr (SIGMOID) return 1.0 / (1.0 + exp(-v));
+        else return bad ? kNanValue : exp(v - mx) / total;
+      };
+      a = score(a);
+      b = score(b);
     }
     double v = p.top == 2 ? a + b : a;
     if (v != v) v = kNanValue;
