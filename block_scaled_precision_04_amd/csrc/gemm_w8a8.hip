@@ -751,7 +751,8 @@ int run_dense_stream(W8A8Args& p, void* ws, hipStream_t st) {
     return d.t == 2 ? launch_stream<1, 2, 8, false, false>(d, p, st) : launch_stream<1, 1, 8, false, false>(d, p, st);
   }
   if (d.mb == 2) return d.r == 4 ? BS_STREAM(2, 4) : BS_STREAM(2, 8);
-  return d.r == 4 ? BS_STREAM(4, 4) : BS_STREAM(4, 8);
+  // (eight blocks a wave: 24 runs of K or more over at most seven grid layers, always a loop)
+  return d.r == 4 ? BS_STREAM(4, 4) : launch_stream<4, 1, 8, true, false>(d, p, st);
 #undef BS_STREAM
 }
 
