@@ -237,7 +237,9 @@ BS_API int bs_prelayout_int8(const void* w, void* out, size_t out_bytes, int N, 
 
 BS_API int bs_unprelayout_int8(const bs_wdesc* d, const void* pre, void* w, bs_stream_t stream) {
   BS_CHECK(d && pre && w, BS_ERR_NULL);
-  BS_CHECK(d->magic == BS_WDESC_MAGIC && d->layout == BS_LAYOUT_INT8 && i8_shape_ok(d->N, d->K), BS_ERR_LAYOUT);
+  BS_CHECK(d->magic == BS_WDESC_MAGIC && d->layout == BS_LAYOUT_INT8 && i8_shape_ok(d->N, d->K) &&
+               d->total_bytes == i8_bytes(d->N, d->K),
+           BS_ERR_LAYOUT);
   BS_CHECK(bs_aligned(w, 16) && bs_aligned(pre, 256), BS_ERR_ALIGN);
   const size_t nchunks = i8_bytes(d->N, d->K) / 16;
   k_i8_pre<<<blocks_for(nchunks), kThreads, 0, static_cast<hipStream_t>(stream)>>>(
