@@ -779,8 +779,11 @@ int launch_split(const W8A8Args& p, int64_t wgs, hipStream_t st) {
 //   t = start + R * (round + steps * step) + x * steps * load,  steps of 128 of K
 // fitted over 20 row counts from 40 to 6000 at twelve N x K, N = 512 .. 34816 and
 // K = 256 .. 17408, weights pooled past the last-level cache: by least squares,
-// then moved a little, with the K splits' below, to the least loss by the choice (0.4%
-// behind the best in the mean of 344 sizes, at worst 13%).  The four shapes with a side of 192 are there
+// then moved a little, with the K splits' below, to the least loss by the choice: 0.4%
+// behind the best in the mean of the 344 sizes of the fit, at worst 13%; on 64 sizes
+// left out of it (M = 65 .. 6000, N and K drawn over the same ranges) 2.4% in the mean, at
+// worst 23%, 53 of them within 3% (the others mostly K below 1000, where 128 x 256 in
+// two workgroups a CU is passed over).  The four shapes with a side of 192 are there
 // for the sizes whose tiles would fill little more than half of the CUs' last round
 // (1024 rows, N = 10240, K = 5120: 54 us, without them 65; 512 rows 43 and 49; 128
 // rows, N = 17408 34 and 40); without them the choice is 2% behind in the mean.
@@ -943,7 +946,8 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
 
 // Row tiles by S / E, the rows an expert would have if they were spread evenly
 // (swept at 256, 128, 64, 32, 16 and 8 experts, S / E from 1/32 to 2048, weights
-// pooled past the last-level cache):
+// pooled past the last-level cache; up to 512 tokens with an even load, from 1024
+// tokens on with a skewed one, where about half of 256 experts get a row):
 //   - less than 16 rows: the weight stream over tiles of 16 rows, waves of eight K
 //     blocks.  64 columns a workgroup in two K groups (256 experts N = 1024 K =
 //     2048: 128 rows 36 us, 5.9 TB/s; 2048 rows 86 us, tiles 94), 32 in four where
@@ -952,11 +956,14 @@ int bs_launch_w8a8(const uint8_t* a, int64_t lda, const float* as, const uint8_t
 //     experts' 1024 rows of N = 512 6.4 us against 7.2);
 //   - few tiles: 64 x 64 (8 experts N = K = 512, 1024 rows 5.2 us, 128 x 256 8);
 //   - up to 47 rows: 64 x 128, three workgroups a CU (256 experts N = 1024 K = 2048,
-//     32 rows 61 us, 128 x 256 69);
+//     32 rows, skewed, 61 us, 128 x 256 69; but 16 rows, even, 102, 128 x 256 95);
 //   - else 128 x 256, two workgroups a CU, so one's stores run under the other's
-//     MFMAs (256 experts N = 1024 K = 2048, 65536 rows 174 us; 256 x 256 190, 128 x
-//     128 229); up to K = 256 128 x 128, three a CU (128 experts N = 512, 65536 rows
-//     27.5 us against 29.8).
+//     MFMAs (256 experts N = 1024 K = 2048, 65536 rows, skewed, 174 us; 256 x 256 190,
+//     128 x 128 229); up to K = 256 128 x 128, three a CU (128 experts N = 512, 65536
+//     rows, skewed, 27.5 us against 29.8).
+// 256 experts N = 1024 K = 2048 with an even load, where all 537 MB of weights are read:
+// 8, 16, 32, 64, 128 and 256 rows an expert 88, 104, 103, 100, 113 and 179 us.  The
+// shapes were not compared there from 32 rows on.
 int bs_launch_w8a8_grouped(const uint8_t* a, int64_t lda, const float* as, const int* offsets, const int* rows,
                            const uint8_t* w, size_t w_stride, const float* wsc, uint16_t* c, int64_t ldc, int S,
                            int Ma, int E, int N, int K, hipStream_t st) {

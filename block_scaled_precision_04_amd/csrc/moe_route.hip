@@ -347,14 +347,18 @@ BS_INLINE void load_logits(const void* base, size_t row, int e0, int E, bool wid
 }
 
 // The quick form: V consecutive experts a lane, the choice by fp32 values.  Without a
-// bias these are the logits themselves (groups' sums of two aside), and the order is
-// exact.  Else they are scores within kTau of the real ones; where two
+// bias these are the logits themselves, and their order is exact (a group's sum of two
+// is one of scores all the same).  Else they are scores within kTau of the real ones;
+// where two
 // values that the order or the border hangs on are closer than that (about one token
 // in 200 of 256 sigmoids), what is close is decided by fp64 values: the groups' sums
 // all anew, or the picks together with up to kMore that follow them, ranked.  (The
 // whole token anew in fp64 is left to rows with a NaN or +inf and to longer runs of
 // close values: the wave takes 8 us, which a launch of 16384 tokens would wait for at
-// its end.)  Weights are fp64 either way, from the picks' logits.
+// its end.)  Weights are computed in fp64 from the picks' logits; only the sum over all
+// experts, which a softmax without renorm divides by, is one of fp32 exponentials, added
+// in fp64: those weights are up to 6 half steps of fp32 off (511 equal logits 4 below the
+// largest, whose differences from it round alike).
 // A lane keeps its values sorted, in lists of four, so a pick is one reduction over
 // the lanes' heads and one shift in the winner's list (16384 tokens, 8 of 256: with
 // every value compared anew in fp64 38 us).
@@ -637,7 +641,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_route(RouteArgs p, bool wid
 // by the waves whose order fp32 leaves open, 3 us of the 12 (with the form above for
 // those 20; all 16 values of a lane anew in fp64 for a border 16).  Where whole tokens
 // are equal sigmoids with a bias, all goes through fp64 (8192 tokens 51 us, a token a
-// wave 36).
+// wave 36).  Its limits are what 16 lanes hold (kManyK + kManyMore candidates, 16
+// experts each) and not where it stops to pay: past them a wave takes one token (16384
+// x 256, cold, us: softmax with 8 picks 8.7, with 9 13.1, with 12 14.8; 384 experts 18,
+// 512 with 10 picks 20).
 constexpr int kManyK = 8, kManyMore = 4;
 static_assert(kManyK + kManyMore <= 16, "a token's candidates are one to a lane");
 // from here on (256 experts, softmax / sigmoids with bias in 8 groups, us: 2048 tokens
@@ -1018,8 +1025,9 @@ BS_INLINE void store_row(void* base, size_t row, int e0, int E, bool wide, const
 // l * V + V - 1 of the row.  The choices' parts go to their experts' places in LDS;
 // where an expert is there twice, one after the other, in the order of j.  Only a
 // softmax over all experts needs the row's logits (DENSE), the others those of the
-// choices.  Bound by the rows' stores and launch (16384 x 256 fp32, 8 choices: 16.8
-// MB written, 8 us).
+// choices.  16384 x 256 fp32, 8 choices, sigmoids 8.1 us, cold 11: launch 2.6, stores of
+// 16.8 MB 3.3, and the VALU, 56% busy with the fp64 exponential, quotients and sums of
+// 8 of a wave's 64 lanes.
 template <int V, bool BF16, bool SIGMOID, bool DENSE>
 __global__ __launch_bounds__(64 * kWaves) void k_moe_route_bwd(RouteBwdArgs p, bool wide) {
   __shared__ __attribute__((aligned(16))) float s_d[kWaves][64 * V];
