@@ -512,7 +512,10 @@ BS_API int moe_route(const void* logits, int64_t ld, int type, const float* bias
  * of the logits' type, [T, E] (ldd elements), every value written (zero where
  * nothing depends on it).  ids as moe_route wrote them; an id outside [0, E) has
  * no part, one that is there twice counts twice.  The choice, and so the bias,
- * has no gradient.  Other arguments and limits as moe_route. */
+ * has no gradient.  A renormalised softmax is taken as the softmax of the chosen
+ * logits, also where a bias chose only such that their scores, and with them
+ * moe_route's weights, are 0 in 64 bits (745 and more below the row's largest).
+ * Other arguments and limits as moe_route. */
 BS_API int moe_route_backward(const float* dweights, const void* logits, int64_t ld, int type, const int32_t* ids,
                               int score, int renorm, float scale, void* dlogits, int64_t ldd, int T, int E, int k,
                               bs_stream_t stream);
